@@ -49,6 +49,9 @@
  *   MONARCH_ERR_NO_MEMORY    the workspace could not be allocated.
  *   MONARCH_ERR_SCRATCH_LIMIT the shape needs more scratch than the static
  *                            array of monarch_attn_fwd_noalloc holds.
+ *   MONARCH_ERR_BAD_INDEX    monarch_attn_dense_decode met a page index or a
+ *                            length outside the cache; reported by
+ *                            monarch_attn_check().
  */
 #ifndef MONARCH_ATTN_H
 #define MONARCH_ATTN_H
@@ -73,6 +76,7 @@ extern "C" {
 #define MONARCH_ERR_DEVICE_TIMEOUT -4
 #define MONARCH_ERR_NO_MEMORY      -5  /* also forced by MONARCH_ATTN_FAIL_ALLOC=1 (see below) */
 #define MONARCH_ERR_SCRATCH_LIMIT  -6
+#define MONARCH_ERR_BAD_INDEX      -7
 
 #define MONARCH_DTYPE_BF16 0
 #define MONARCH_DTYPE_F32  1
@@ -230,6 +234,104 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
                                  const void* dout, void* dq, void* dk, void* dv, int B, int H,
                                  int b1, int b2, int d, int T, int c1, int c2,
                                  cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Exact softmax attention, for the layers of a model that stay dense (the
+ * pages replace some layers and keep others, MonarchAttention OpenReview
+ * discussion), for causal masks and single-token decoding, which
+ * MonarchAttention does not support (MonarchAttention AI summary,
+ * "Limitations"), and rotary positions for q and k.
+ *
+ * Tensors are (B, heads, N, d) with the d elements of a token contiguous and
+ * any other strides: `strides` is a host array of three element strides
+ * (batch, head, token) per tensor, in the order of the arguments, or NULL
+ * when every tensor is contiguous.  Inputs may repeat (stride 0); the
+ * elements of an output may not, and an output must not overlap an input or
+ * another output (address ranges from the first element to the last).
+ * Pointers are aligned to their elements; rows that are 16-byte aligned
+ * (pointer and strides) take the faster kernels.  d is 1 to 256.  Every call
+ * is asynchronous on `stream`, works on the current device, allocates
+ * nothing and keeps nothing: the caller passes the workspace, so calls on
+ * several streams and captured graphs are independent as long as their
+ * workspaces are.  Deterministic: no atomics in any sum.
+ * ------------------------------------------------------------------------- */
+
+/* out = softmax(scale q k^T over the visible keys) v, and lse, the natural
+ * log of the sum of exponentials, (B, H, Nq) contiguous.
+ * q, out: (B, H, Nq, d); k, v: (B, Hkv, Nk, d), H a multiple of Hkv (query
+ * head h reads head h / (H / Hkv)); strides: q, k, v, out.  Key j is visible
+ * to query i of batch b when j < k_lens[b] (device, B ints, or NULL; values
+ * outside [0, Nk] count as the nearer end) and, if causal, j <= i + Nk - Nq.
+ * A row without a visible key gets out = 0 and lse = -inf.  Keys past the
+ * length may hold anything (NaN included); keys hidden by `causal` alone must
+ * be finite.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
+ * for the product with v, sums are fp32.  scale > 0. */
+MONARCH_API int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* v,
+                                       void* out, float* lse, int B, int H, int Hkv, int Nq,
+                                       int Nk, int d, const long long* strides, int causal,
+                                       const int* k_lens, float scale, cudaStream_t stream);
+
+/* Gradients of sum(out * dout) with respect to q, k and v; the probabilities
+ * are recomputed from q, k and lse.  out and lse: what
+ * monarch_attn_dense_fwd gave for the same arguments.  strides: q, k, v, out,
+ * dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
+ * does a query without a visible key.  workspace: device, 16-byte aligned,
+ * monarch_attn_dense_bwd_workspace_bytes. */
+MONARCH_API int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* v,
+                                       const void* out, const float* lse, const void* dout,
+                                       void* dq, void* dk, void* dv, int B, int H, int Hkv,
+                                       int Nq, int Nk, int d, const long long* strides,
+                                       int causal, const int* k_lens, float scale,
+                                       void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+MONARCH_API size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq);
+
+/* Attention of one new token per sequence over a paged cache.
+ * q, out: (B, H, d); k_cache, v_cache: (n_pages, Hkv, page_size, d); key j of
+ * sequence b is row j % page_size of page page_table[b][j / page_size]
+ * (device, (B, max_pages) contiguous; entries past the sequence's pages are
+ * not read).  lens: device, B ints, the keys of each sequence, 0 to
+ * max_pages * page_size; a sequence of length 0 gets out = 0, lse = -inf.
+ * lse: (B, H).  strides: q (batch, head, unused), k_cache and v_cache (page,
+ * head, row), out (batch, head, unused).  Rows of a page past the length may
+ * hold anything.  The cache is split over its length and joined in order.  A
+ * page index outside [0, n_pages) contributes a zero key and value, a length
+ * outside its range counts as the nearer end, and monarch_attn_check then
+ * reports MONARCH_ERR_BAD_INDEX.  workspace: device, 16-byte aligned,
+ * monarch_attn_dense_decode_workspace_bytes. */
+MONARCH_API int monarch_attn_dense_decode(int dtype, const void* q, const void* k_cache,
+                                          const void* v_cache, const int* page_table,
+                                          const int* lens, void* out, float* lse, int B, int H,
+                                          int Hkv, int d, int n_pages, int page_size,
+                                          int max_pages, const long long* strides, float scale,
+                                          void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream);
+MONARCH_API size_t monarch_attn_dense_decode_workspace_bytes(int dtype, int B, int H, int Hkv,
+                                                             int d, int page_size,
+                                                             int max_pages);
+
+/* Rotary positions: pairs (a, b) of each token's channels become
+ *   magnitude (a cos t - b sin t),  magnitude (b cos t + a sin t),
+ * t = position * frequency of the pair (inverse = 1: t negated, which is the
+ * gradient with respect to the input).  The first sum(axis_dims) channels are
+ * cut into one section per position axis (1 to 4 axes, even sizes); inside a
+ * section of n channels pair r is (2r, 2r + 1) if interleaved, else
+ * (r, r + n/2).  The other channels are copied.
+ * q, q_out: (B, H, N, d); k, k_out: (B, Hkv, N, d); H or Hkv may be 0 (no such
+ * tensor).  strides: q, q_out, k, k_out.  An output may be its own input
+ * (rotated in place).  Positions: `grid` (host, one size per axis, product N:
+ * token n is that place in raster order, last axis fastest) or `positions`
+ * (device, ints, (n_axes, N) contiguous per batch, batches
+ * positions_batch_stride elements apart, 0 to share them); one of them is
+ * NULL.  freqs: host, one angular frequency per pair, axis after axis; the
+ * angles are reduced in 64 bits. */
+MONARCH_API int monarch_attn_rotary(int dtype, const void* q, const void* k, void* q_out,
+                                    void* k_out, int B, int H, int Hkv, int N, int d,
+                                    const long long* strides, int n_axes, const int* axis_dims,
+                                    const int* grid, const int* positions,
+                                    long long positions_batch_stride, const double* freqs,
+                                    double magnitude, int interleaved, int inverse,
+                                    cudaStream_t stream);
 
 /* Bytes of device workspace a call with these arguments uses (0 on invalid
  * arguments).  dtype is MONARCH_DTYPE_BF16 or MONARCH_DTYPE_F32. */

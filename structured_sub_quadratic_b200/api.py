@@ -7,7 +7,10 @@ and a missing library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import math
 import os
 
 import torch
@@ -21,12 +24,14 @@ MONARCH_ERR_CUDA = -3
 MONARCH_ERR_DEVICE_TIMEOUT = -4
 MONARCH_ERR_NO_MEMORY = -5
 MONARCH_ERR_SCRATCH_LIMIT = -6
+MONARCH_ERR_BAD_INDEX = -7
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
 LAYOUTS = {"fh,w": 0, "w,fh": 1, "f,hw": 2, "hw,f": 3, "fw,h": 4, "h,fw": 5}
 
 # Every symbol the header declares, with its ctypes signature.
 _I, _P, _Z = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_L, _F, _D = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
 _SIZES = [_I] * 8  # B, H, b1, b2, d, T, c1, c2
 SIGNATURES = {
     "monarch_attn_fwd": (_I, [_P, _P, _P, _P, *_SIZES, _P]),
@@ -38,6 +43,13 @@ SIGNATURES = {
     "monarch_attn_fwd_padded": (_I, [_I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                      _I, _P]),
     "monarch_attn_bwd": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, *_SIZES, _P]),
+    "monarch_attn_dense_fwd": (_I, [_I, _P, _P, _P, _P, _P, *[_I] * 6, _P, _I, _P, _F, _P]),
+    "monarch_attn_dense_bwd": (_I, [_I, *[_P] * 9, *[_I] * 6, _P, _I, _P, _F, _P, _Z, _P]),
+    "monarch_attn_dense_bwd_workspace_bytes": (_Z, [_I, _I, _I]),
+    "monarch_attn_dense_decode": (_I, [_I, *[_P] * 7, *[_I] * 7, _P, _F, _P, _Z, _P]),
+    "monarch_attn_dense_decode_workspace_bytes": (_Z, [_I] * 7),
+    "monarch_attn_rotary": (_I, [_I, *[_P] * 4, *[_I] * 5, _P, _I, _P, _P, _P, _L, _P, _D, _I,
+                                 _I, _P]),
     "monarch_attn_workspace_bytes": (_Z, [*_SIZES, _I]),
     "monarch_attn_release_workspace": (None, []),
     "monarch_attn_check": (_I, [_P]),
@@ -205,9 +217,15 @@ def video_blocks(f, h, w, layout):
     return b1, b2
 
 
-def monarch_attn_fwd_video(q, k, v, f, h, w, layout, T, c1=1, c2=1, out=None, stream=None):
+def monarch_attn_fwd_video(q, k, v, f, h, w, layout, T, c1=1, c2=1, out=None, stream=None,
+                           rotary=None):
     """Forward pass on a video latent (B, H, f*h*w, d) in raster token order,
-    with the Monarch blocks aligned to ``layout`` (a key of LAYOUTS)."""
+    with the Monarch blocks aligned to ``layout`` (a key of LAYOUTS).
+
+    ``rotary``: keyword arguments of ``monarch_attn_rotary`` (``axis_dims`` of
+    the three axes f, h and w, and any of ``interleaved``, ``base`` and
+    ``scaling``) that q and k are rotated with first, by their place in the
+    latent; q and k are left as they are."""
     lib = load_library()
     if layout not in LAYOUTS:
         raise ValueError(f"unknown layout {layout!r}; expected one of {sorted(LAYOUTS)}")
@@ -220,6 +238,8 @@ def monarch_attn_fwd_video(q, k, v, f, h, w, layout, T, c1=1, c2=1, out=None, st
     dtype = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(q.dtype)
     if dtype is None:
         raise ValueError(f"unsupported dtype {q.dtype}")
+    if rotary is not None:
+        q, k = monarch_attn_rotary(q, k, grid=(f, h, w), stream=stream, **rotary)
     if out is None:
         out = torch.empty_like(q)
     _check(lib.monarch_attn_fwd_video(dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -240,6 +260,277 @@ def monarch_attn_fwd_host(q, k, v, out, b1, b2, T, c1=1, c2=1, stream=None):
                                      out.data_ptr(), B, H, b1, b2, d, T, c1, c2,
                                      _stream_ptr(stream)))
     return out
+
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """`device` current and, if given, `stream` too: what is allocated inside
+    belongs to the stream that uses it."""
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _scope(t, stream):
+    """Context of a call on t's device (nothing to do where it is current)."""
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {t.device}")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _on(t.device, stream)
+
+
+def _dense_dtype(name, like, *tensors):
+    """The dtype code of `like` after checking that each tensor shares its
+    dtype and CUDA device and has contiguous channels."""
+    dtype = _DTYPES.get(like.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported dtype {like.dtype}")
+    for t in (like, *tensors):
+        if t.dtype != like.dtype or not t.is_cuda or t.device != like.device:
+            raise ValueError(f"{name} must be CUDA tensors of one dtype on one device")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name} must have contiguous channels (last stride 1)")
+    return dtype
+
+
+def _int_tensor(name, t, device, shape):
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {shape} on {device}")
+    return t.data_ptr()
+
+
+def _strides(*tensors):
+    """Batch, head and token strides of (B, H, N, d) tensors for the C ABI."""
+    return (_L * (3 * len(tensors)))(*(s for t in tensors for s in t.stride()[:3]))
+
+
+def _dense_dims(q, k, v, scale):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected (B, H, Nq, d) and (B, Hkv, Nk, d) tensors")
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if k.shape != (B, Hkv, Nk, d) or v.shape != k.shape:
+        raise ValueError("k and v must be (B, Hkv, Nk, d) with q's B and d")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"{H} query heads cannot share {Hkv} key/value heads")
+    return B, H, Hkv, Nq, Nk, d, 1.0 / math.sqrt(d) if scale is None else scale
+
+
+def monarch_attn_dense_fwd(q, k, v, causal=False, k_lens=None, scale=None, out=None,
+                           stream=None):
+    """Exact softmax attention: (out, lse) of q (B, H, Nq, d) over k and v
+    (B, Hkv, Nk, d), H a multiple of Hkv, in any strides with contiguous
+    channels.
+
+    ``causal``: query i sees the keys up to i + Nk - Nq.  ``k_lens``: int32
+    (B,) on the device, the keys of each sequence that count; what lies past
+    them is never used.  A row that sees no key gets out = 0, lse = -inf.
+    ``scale`` defaults to 1/sqrt(d).  lse is fp32 (B, H, Nq), for
+    ``monarch_attn_dense_bwd``.
+    """
+    lib = load_library()
+    B, H, Hkv, Nq, Nk, d, scale = _dense_dims(q, k, v, scale)
+    dtype = _dense_dtype("q, k, v and out", q, k, v, *(() if out is None else (out,)))
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    lens = None if k_lens is None else _int_tensor("k_lens", k_lens, q.device, (B,))
+    with _scope(q, stream):
+        if out is None:
+            out = torch.empty_like(q) if _own_memory(q) else q.new_empty(q.shape)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        _check(lib.monarch_attn_dense_fwd(
+            dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
+            Hkv, Nq, Nk, d, _strides(q, k, v, out), bool(causal), lens, scale,
+            _stream_ptr(stream)))
+    return out, lse
+
+
+def monarch_attn_dense_bwd(q, k, v, out, lse, dout, causal=False, k_lens=None, scale=None,
+                           stream=None):
+    """Gradients (dq, dk, dv) of sum(out * dout) for the exact attention of
+    ``monarch_attn_dense_fwd``, whose out and lse it takes with the same other
+    arguments.  The probabilities are recomputed tile by tile; a key/value
+    head's gradient sums over the query heads that share it."""
+    lib = load_library()
+    B, H, Hkv, Nq, Nk, d, scale = _dense_dims(q, k, v, scale)
+    dtype = _dense_dtype("q, k, v, out and dout", q, k, v, out, dout)
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have q's shape")
+    if lse.dtype != torch.float32 or lse.shape != (B, H, Nq) or lse.device != q.device \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be the contiguous fp32 (B, H, Nq) tensor of the forward pass")
+    lens = None if k_lens is None else _int_tensor("k_lens", k_lens, q.device, (B,))
+    with _scope(q, stream):
+        dq, dk, dv = (torch.empty_like(t) if _own_memory(t) else
+                      torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        need = lib.monarch_attn_dense_bwd_workspace_bytes(B, H, Nq)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _check(lib.monarch_attn_dense_bwd(
+            dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Nq, Nk, d,
+            _strides(q, k, v, out, dout, dq, dk, dv), bool(causal), lens, scale, ws.data_ptr(),
+            need, _stream_ptr(stream)))
+    return dq, dk, dv
+
+
+def _own_memory(t):
+    """No element of t repeats another (no expanded dimension)."""
+    return all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape))
+
+
+def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None, out=None,
+                              stream=None):
+    """Exact attention of one new token per sequence over a paged cache:
+    (out, lse) of q (B, H, d).
+
+    k_cache, v_cache: (pages, Hkv, page_size, d) in any strides with
+    contiguous channels (a (pages, page_size, Hkv, d) cache is passed as its
+    transpose(1, 2)).  page_table: int32 (B, max_pages); key j of sequence b is
+    row j % page_size of page page_table[b, j // page_size].  lens: int32
+    (B,), the keys of each sequence (0: out = 0, lse = -inf).  lse is fp32
+    (B, H).  Pages and lengths are checked on the device: ``check`` raises
+    MONARCH_ERR_BAD_INDEX after one that lay outside the cache.
+    """
+    lib = load_library()
+    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("expected q (B, H, d) and caches (pages, Hkv, page_size, d)")
+    B, H, d = q.shape
+    pages, Hkv, page_size, dk = k_cache.shape
+    if dk != d or Hkv < 1 or H % Hkv:
+        raise ValueError("the caches must have q's d and a divisor of its heads")
+    dtype = _dense_dtype("q, k_cache, v_cache and out", q, k_cache, v_cache,
+                         *(() if out is None else (out,)))
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (B, max_pages)")
+    max_pages = page_table.shape[1]
+    table = _int_tensor("page_table", page_table, q.device, (B, max_pages))
+    lens = _int_tensor("lens", lens, q.device, (B,))
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _scope(q, stream):
+        if out is None:
+            out = torch.empty_like(q) if _own_memory(q) else q.new_empty(q.shape)
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        need = lib.monarch_attn_dense_decode_workspace_bytes(dtype, B, H, Hkv, d, page_size,
+                                                             max_pages)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        sq, so, sk, sv = q.stride(), out.stride(), k_cache.stride(), v_cache.stride()
+        strides = (_L * 12)(sq[0], sq[1], 0, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], so[0],
+                            so[1], 0)
+        _check(lib.monarch_attn_dense_decode(
+            dtype, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, lens,
+            out.data_ptr(), lse.data_ptr(), B, H, Hkv, d, pages, page_size, max_pages, strides,
+            scale, ws.data_ptr(), need, _stream_ptr(stream)))
+    return out, lse
+
+
+def rotary_frequencies(axis_dims, base=10000.0, scaling=None):
+    """(angular frequency of each rotated pair, magnitude), axis after axis.
+
+    Pair r of an axis with n channels turns base^(-2r/n) radians per position.
+    ``scaling`` stretches them to a longer context by a factor s:
+    ``("linear", s)`` divides every frequency by s; ``("ntk", s)`` raises the
+    base by s^(n/(n-2)), which leaves the fastest pair and slows the last one
+    s-fold; ``("parts", s, original, slow, fast)`` keeps the pairs that turn
+    more than ``fast`` times over the original context, divides by s those
+    that turn less than ``slow`` times, blends linearly between, and scales
+    the rotated channels by 0.1 ln(s) + 1 (s >= 1).
+    """
+    kind = None if scaling is None else scaling[0]
+    if kind is not None and (len(scaling) != {"linear": 2, "ntk": 2, "parts": 5}.get(kind)
+                             or not scaling[1] > 0):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not base > 0:
+        raise ValueError("base must be positive")
+    freqs = []
+    for n in axis_dims:
+        b = base * scaling[1] ** (n / max(n - 2, 1)) if kind == "ntk" else base
+        for r in range(n // 2):
+            f = b ** (-2 * r / n)
+            if kind == "linear":
+                f /= scaling[1]
+            elif kind == "parts":
+                _, s, original, slow, fast = scaling
+                if not fast > slow or s < 1:
+                    raise ValueError("parts scaling needs fast > slow and a factor >= 1")
+                keep = min(1.0, max(0.0, (original * f / (2 * math.pi) - slow) / (fast - slow)))
+                f *= keep + (1 - keep) / s
+            freqs.append(f)
+    return freqs, 0.1 * math.log(scaling[1]) + 1 if kind == "parts" else 1.0
+
+
+@functools.lru_cache(maxsize=64)
+def _rotary_args(axis_dims, base, scaling):
+    """ctypes forms of axis_dims and the frequencies (a function of the arguments alone)."""
+    freqs, magnitude = rotary_frequencies(axis_dims, base, scaling)
+    return ((_I * len(axis_dims))(*axis_dims), (_D * len(freqs))(*freqs), magnitude)
+
+
+def monarch_attn_rotary(q, k=None, positions=None, *, axis_dims=None, grid=None,
+                        interleaved=False, base=10000.0, scaling=None, inverse=False, q_out=None,
+                        k_out=None, stream=None):
+    """Rotary positions: (rotated q, rotated k) of q (B, H, N, d) and k (B,
+    Hkv, N, d) (k may be None), in any strides with contiguous channels.
+
+    The first sum(axis_dims) channels are cut into one section per position
+    axis (default: all d, one axis); the pairs of a section are neighbours if
+    ``interleaved``, else the same place of its two halves; the other channels
+    are copied.  Positions: ``grid``, one size per axis with product N (token
+    n is that place in raster order: (f, h, w) for a video latent), or
+    ``positions``, int32 (N,), (axes, N) or (B, axes, N) on the device.
+    Frequencies: see ``rotary_frequencies``.  ``inverse`` turns the other way:
+    the gradient with respect to q and k of a gradient with respect to the
+    outputs.  ``q_out`` and ``k_out`` may be q and k (in place).
+    """
+    lib = load_library()
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0]
+                                           or k.shape[2:] != q.shape[2:])):
+        raise ValueError("expected q (B, H, N, d) and k (B, Hkv, N, d)")
+    B, H, N, d = q.shape
+    axis_dims = (d,) if axis_dims is None else tuple(axis_dims)
+    if not 1 <= len(axis_dims) <= 4 or any(n < 2 or n % 2 for n in axis_dims) \
+            or sum(axis_dims) > d:
+        raise ValueError("axis_dims must be one to four even sizes within d channels")
+    given = [t for t in (k, q_out, k_out) if t is not None]
+    dtype = _dense_dtype("q, k and the outputs", q, *given)
+    if (q_out is not None and q_out.shape != q.shape) or \
+            (k_out is not None and (k is None or k_out.shape != k.shape)):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    if (grid is None) == (positions is None):
+        raise ValueError("one of grid and positions is needed")
+    where, step, sizes = None, 0, None
+    if grid is not None:
+        if len(grid) != len(axis_dims) or math.prod(grid) != N:
+            raise ValueError("grid must have one size per axis, with product N")
+        sizes = (_I * len(grid))(*grid)
+    else:
+        shape = (len(axis_dims), N)
+        if positions.dim() == 1 and len(axis_dims) == 1:
+            shape = (N,)
+        elif positions.dim() == 3:
+            shape, step = (B, *shape), len(axis_dims) * N
+        where = _int_tensor("positions", positions, q.device, shape)
+    dims, freqs, magnitude = _rotary_args(axis_dims, base, scaling)
+    with _scope(q, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q) if _own_memory(q) else q.new_empty(q.shape)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k) if _own_memory(k) else k.new_empty(k.shape)
+        if k is None:
+            heads, kp, kop, strides = 0, None, None, _strides(q, q_out, q, q_out)
+        else:
+            heads, kp, kop = k.shape[1], k.data_ptr(), k_out.data_ptr()
+            strides = _strides(q, q_out, k, k_out)
+        _check(lib.monarch_attn_rotary(
+            dtype, q.data_ptr(), kp, q_out.data_ptr(), kop, B, H, heads, N, d, strides,
+            len(axis_dims), dims, sizes, where, step, freqs, magnitude, bool(interleaved),
+            bool(inverse), _stream_ptr(stream)))
+    return q_out, k_out
 
 
 def workspace_bytes(B, H, b1, b2, d, T, c1=1, c2=1, dtype=torch.bfloat16):

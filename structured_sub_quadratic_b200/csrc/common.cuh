@@ -148,5 +148,8 @@ __device__ __forceinline__ float dot_row(const float* __restrict__ sq,
 // instead of trapping; the host reads it through monarch_attn_check().
 // ---------------------------------------------------------------------------
 #define MONARCH_DEVICE_TIMEOUT_FLAG 1
+// a page table entry or a sequence length outside the cache (paged decode);
+// set only where nothing else is recorded
+#define MONARCH_DEVICE_BAD_INDEX_FLAG 4
 
 }  // namespace monarch

@@ -25,4 +25,10 @@ Bf16Kernels choose_bf16_kernels(const Problem& pb);
 // a timeout.  Nothing is allocated for it.  Returns a MONARCH_* status.
 int device_status_word(int dev, int** out);
 
+// Keeps the error's text for monarch_attn_strerror; returns MONARCH_ERR_CUDA.
+int cuda_failure(cudaError_t e);
+
+// This host thread's launch count of the most recent call.
+int* launch_counter();
+
 }  // namespace monarch

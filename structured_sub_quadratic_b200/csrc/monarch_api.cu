@@ -296,6 +296,10 @@ int device_status_word(int dev, int** out) {
   return status_word_locked(dev, out);
 }
 
+int cuda_failure(cudaError_t e) { return record_cuda(e); }
+
+int* launch_counter() { return &t_launches; }
+
 }  // namespace monarch
 
 extern "C" {
@@ -701,7 +705,8 @@ int monarch_attn_check(cudaStream_t stream) {
     return record_cuda(e);
   if (flag) {
     if ((e = cudaMemset(p, 0, sizeof(int))) != cudaSuccess) return record_cuda(e);
-    return MONARCH_ERR_DEVICE_TIMEOUT;
+    return flag == MONARCH_DEVICE_BAD_INDEX_FLAG ? MONARCH_ERR_BAD_INDEX
+                                                 : MONARCH_ERR_DEVICE_TIMEOUT;
   }
   return MONARCH_OK;
 }
@@ -720,6 +725,9 @@ const char* monarch_attn_strerror(int status) {
     case MONARCH_ERR_SCRATCH_LIMIT:
       return "the shape needs more scratch than the 64 MiB static array of "
              "monarch_attn_fwd_noalloc holds";
+    case MONARCH_ERR_BAD_INDEX:
+      return "a page table entry or a sequence length lay outside the cache; its keys were left "
+             "out";
     default: return "unknown status";
   }
 }
