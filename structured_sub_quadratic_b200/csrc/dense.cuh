@@ -51,6 +51,13 @@ cudaError_t dense_simt_backward(const T* q, const T* k, const T* v, const T* out
                                 float* delta, const DenseProblem& pb, cudaStream_t stream,
                                 int* launches);
 
+// Tensor-core kernels (dense_tc.cu): bf16, d a multiple of 8 up to 128, rows
+// of 16-byte alignment.
+bool dense_tc_rows(const void* p, const HeadStrides& s, int N, int d);
+cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
+                             const DenseProblem& pb, int* status, cudaStream_t stream,
+                             int* launches);
+
 // delta[b, h, i] = sum_x dout out, (B, H, Nq) contiguous.
 template <typename T>
 cudaError_t dense_delta(const T* out, const T* dout, float* delta, const DenseProblem& pb,

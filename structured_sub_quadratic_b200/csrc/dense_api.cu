@@ -81,6 +81,13 @@ HeadStrides strides_of(const long long* s, int which, long B, long H, long N, lo
   return r;
 }
 
+// The current device's status word.
+int status_word(int** out) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? monarch::device_status_word(dev, out) : monarch::cuda_failure(e);
+}
+
 bool dtype_ok(int dtype) { return dtype == MONARCH_DTYPE_BF16 || dtype == MONARCH_DTYPE_F32; }
 
 // Sizes of a dense call; tiles of 32 rows of every head must fit a grid.
@@ -148,15 +155,24 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
                  ranges_meet(out, o.extent() * elt, lse, lse_bytes)))
     return MONARCH_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return MONARCH_ERR_INVALID_ARG;
-  const cudaError_t e =
-      dtype == MONARCH_DTYPE_BF16
-          ? monarch::dense_simt_forward<bf16>(
-                static_cast<const bf16*>(q), static_cast<const bf16*>(k),
-                static_cast<const bf16*>(v), static_cast<bf16*>(out), lse, pb, stream, launches)
-          : monarch::dense_simt_forward<float>(
-                static_cast<const float*>(q), static_cast<const float*>(k),
-                static_cast<const float*>(v), static_cast<float*>(out), lse, pb, stream,
-                launches);
+  cudaError_t e;
+  if (dtype == MONARCH_DTYPE_F32) {
+    e = monarch::dense_simt_forward<float>(
+        static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
+        static_cast<float*>(out), lse, pb, stream, launches);
+  } else if (Nq > 0 && Nk > 0 && monarch::dense_tc_rows(q, pb.q, Nq, d) &&
+             monarch::dense_tc_rows(k, pb.k, Nk, d) && monarch::dense_tc_rows(v, pb.v, Nk, d) &&
+             monarch::dense_tc_rows(out, pb.out, Nq, d)) {
+    int* status = nullptr;
+    if ((st = status_word(&status)) != MONARCH_OK) return st;
+    e = monarch::dense_tc_forward(static_cast<const bf16*>(q), static_cast<const bf16*>(k),
+                                  static_cast<const bf16*>(v), static_cast<bf16*>(out), lse, pb,
+                                  status, stream, launches);
+  } else {
+    e = monarch::dense_simt_forward<bf16>(
+        static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),
+        static_cast<bf16*>(out), lse, pb, stream, launches);
+  }
   return e == cudaSuccess ? MONARCH_OK : monarch::cuda_failure(e);
 }
 
@@ -319,12 +335,10 @@ int monarch_attn_dense_decode(int dtype, const void* q, const void* k_cache, con
   pb.v_n = sv.n;
   pb.table = page_table;
   pb.lens = lens;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return monarch::cuda_failure(e);
   int* status = nullptr;
-  if ((st = monarch::device_status_word(dev, &status)) != MONARCH_OK) return st;
-  e = dtype == MONARCH_DTYPE_BF16
+  if ((st = status_word(&status)) != MONARCH_OK) return st;
+  const cudaError_t e =
+      dtype == MONARCH_DTYPE_BF16
           ? monarch::decode_forward<bf16>(static_cast<const bf16*>(q),
                                           static_cast<const bf16*>(k_cache),
                                           static_cast<const bf16*>(v_cache),
