@@ -57,6 +57,10 @@ bool dense_tc_rows(const void* p, const HeadStrides& s, int N, int d);
 cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
                              const DenseProblem& pb, int* status, cudaStream_t stream,
                              int* launches);
+cudaError_t dense_tc_backward(const bf16* q, const bf16* k, const bf16* v, const bf16* out,
+                              const float* lse, const bf16* dout, bf16* dq, bf16* dk, bf16* dv,
+                              float* delta, const DenseProblem& pb, int* status,
+                              cudaStream_t stream, int* launches);
 
 // delta[b, h, i] = sum_x dout out, (B, H, Nq) contiguous.
 template <typename T>

@@ -226,18 +226,31 @@ int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* 
   }
   if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return MONARCH_ERR_INVALID_ARG;
   float* delta = static_cast<float*>(workspace);
-  const cudaError_t e =
-      dtype == MONARCH_DTYPE_BF16
-          ? monarch::dense_simt_backward<bf16>(
-                static_cast<const bf16*>(q), static_cast<const bf16*>(k),
-                static_cast<const bf16*>(v), static_cast<const bf16*>(out), lse,
-                static_cast<const bf16*>(dout), static_cast<bf16*>(dq), static_cast<bf16*>(dk),
-                static_cast<bf16*>(dv), delta, pb, stream, launches)
-          : monarch::dense_simt_backward<float>(
-                static_cast<const float*>(q), static_cast<const float*>(k),
-                static_cast<const float*>(v), static_cast<const float*>(out), lse,
-                static_cast<const float*>(dout), static_cast<float*>(dq),
-                static_cast<float*>(dk), static_cast<float*>(dv), delta, pb, stream, launches);
+  cudaError_t e;
+  if (dtype == MONARCH_DTYPE_F32) {
+    e = monarch::dense_simt_backward<float>(
+        static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
+        static_cast<const float*>(out), lse, static_cast<const float*>(dout),
+        static_cast<float*>(dq), static_cast<float*>(dk), static_cast<float*>(dv), delta, pb,
+        stream, launches);
+    return e == cudaSuccess ? MONARCH_OK : monarch::cuda_failure(e);
+  }
+  const bf16 *bq = static_cast<const bf16*>(q), *bk = static_cast<const bf16*>(k),
+             *bv = static_cast<const bf16*>(v), *bo = static_cast<const bf16*>(out),
+             *bg = static_cast<const bf16*>(dout);
+  bf16 *gq = static_cast<bf16*>(dq), *gk = static_cast<bf16*>(dk), *gv = static_cast<bf16*>(dv);
+  if (Nq > 0 && Nk > 0 && monarch::dense_tc_rows(q, pb.q, Nq, d) &&
+      monarch::dense_tc_rows(k, pb.k, Nk, d) && monarch::dense_tc_rows(v, pb.v, Nk, d) &&
+      monarch::dense_tc_rows(dout, pb.dout, Nq, d) && monarch::dense_tc_rows(dq, pb.dq, Nq, d) &&
+      monarch::dense_tc_rows(dk, pb.dk, Nk, d) && monarch::dense_tc_rows(dv, pb.dv, Nk, d)) {
+    int* status = nullptr;
+    if ((st = status_word(&status)) != MONARCH_OK) return st;
+    e = monarch::dense_tc_backward(bq, bk, bv, bo, lse, bg, gq, gk, gv, delta, pb, status, stream,
+                                   launches);
+  } else {
+    e = monarch::dense_simt_backward<bf16>(bq, bk, bv, bo, lse, bg, gq, gk, gv, delta, pb, stream,
+                                           launches);
+  }
   return e == cudaSuccess ? MONARCH_OK : monarch::cuda_failure(e);
 }
 

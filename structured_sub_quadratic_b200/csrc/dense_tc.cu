@@ -395,6 +395,556 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Backward.  The probabilities are recomputed from q, k and lse; delta is the
+// row sum of dO O.  Two kernels, so that no sum needs atomics: one owns a tile
+// of keys and walks the queries (dK, dV: four products a tile), the other a
+// tile of queries and walks the keys (dQ: three).  In both, eight warps hold
+// the score tile with two threads per TMEM lane (64 columns each: warps 0-3
+// the first, 4-7 the second half), warp 8 issues TMA and warp 9 the products.
+// ---------------------------------------------------------------------------
+struct BwdArgs {
+  const float* lse;
+  const float* delta;
+  DenseProblem pb;
+  int tiles;  // 128-row tiles of a head
+  int* status;
+};
+
+constexpr int kBwdThreads = 320;
+
+// The 64 columns of a thread as bf16 pairs, over its own half of a score tile.
+__device__ __forceinline__ void store_half(uint32_t taddr, const float (&x)[64]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]);
+    tmem_st16(taddr + c * 16, pk);
+  }
+}
+
+__device__ __forceinline__ void load_half(uint32_t taddr, float (&x)[64]) {
+  float t[2][32];
+  tmem_ld32(taddr, t[0]);
+  tmem_ld32(taddr + 32, t[1]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 64; ++e) x[e] = t[e >> 5][e & 31];
+}
+
+// D[tmem] (+)= W X, W's columns 0-63 and 64-127 as store_half left them.
+template <int D>
+__device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t w, uint64_t x,
+                                           bool accumulate) {
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    mma_bf16_ts(tmem, w + (kk >> 2) * 64 + (kk & 3) * 8, x + ((kk * 16 * 128) >> 4),
+                idesc_bf16(kTile, D, true), accumulate || kk > 0 ? 1u : 0u);
+}
+
+// Row r of a D-wide accumulator times `f`, as bf16, into a swizzled tile.
+template <int D>
+__device__ __forceinline__ void accumulator_row(uint8_t* tile, int r, uint32_t taddr, float f,
+                                                bool any) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    if (any) {
+      tmem_ld32(taddr + c * 32, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * f : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *row_unit(tile, r, c * 4 + u) =
+          make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                     pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
+                     pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+  }
+}
+
+template <int D>
+struct BwdLayout {
+  static constexpr int kCh = D / 64, kStages = 2;
+  static constexpr int kTileBytes = kCh * kChunk;
+  static constexpr int kAOff = 0;                      // the two tiles that stay
+  static constexpr int kBOff = kAOff + kTileBytes;
+  static constexpr int kXOff = kBOff + kTileBytes;     // the two that are streamed
+  static constexpr int kYOff = kXOff + kStages * kTileBytes;
+  static constexpr int kRowOff = kYOff + kStages * kTileBytes;  // float [stages][2][128]
+  static constexpr int kBarOff = kRowOff + kStages * 2 * kTile * 4;
+  static constexpr int kBytes = kBarOff + 32 * 8;
+  // S and dP (P and dS over them), then the accumulators
+  static constexpr uint32_t kTmemCols = 512, kDPCol = 128, kAccCol = 256;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// dK and dV of 128 keys of a key/value head.  With keys as the rows:
+//   S^T = K Q^T, P^T = exp(scale S^T - lse), dV += P^T dO,
+//   dP^T = V dO^T, dS^T = P^T (dP^T - delta), dK += dS^T Q (times scale).
+// P^T and dS^T are written over S^T and dP^T and read as A operands, so
+// exponentials of one tile run beside dK and dP of the tile before, and dS
+// beside dV and the next S.  The query heads of the group follow one another
+// in the same accumulators.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    dense_dkv_tc_kernel(const __grid_constant__ TileMap mq, const __grid_constant__ TileMap mk,
+                        const __grid_constant__ TileMap mv, const __grid_constant__ TileMap mg,
+                        const __grid_constant__ TileMap mdk, const __grid_constant__ TileMap mdv,
+                        const __grid_constant__ BwdArgs a) {
+  using L = BwdLayout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) atomicExch(a.status, 2);
+    return;
+  }
+  const DenseProblem& pb = a.pb;
+  // causal: the first keys, which most queries see, first
+  const int heads = pb.B * pb.Hkv;
+  const int tile = pb.causal ? blockIdx.x / heads : blockIdx.x % a.tiles;
+  const int bh = pb.causal ? blockIdx.x % heads : blockIdx.x / a.tiles;
+  const int hk = bh % pb.Hkv, b = bh / pb.Hkv, group = pb.H / pb.Hkv;
+  const int k0 = tile * kTile, shift = pb.Nk - pb.Nq;
+  const int len = dense_len(pb, b);
+  const int first = pb.causal ? max(0, k0 - shift) / kTile : 0;  // query tile
+  const int per = k0 < len ? max(0, (pb.Nq + kTile - 1) / kTile - first) : 0;
+  const int n = per * group;
+
+  float* rows = reinterpret_cast<float*>(smem + L::kRowOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;   // [stages]: Q and the row statistics
+  uint64_t* g_full = bars + 3;   // [stages]: dO
+  uint64_t* empty = bars + 5;    // [stages]
+  uint64_t* s_full = bars + 7;
+  uint64_t* dp_full = bars + 8;
+  uint64_t* p_full = bars + 9;
+  uint64_t* ds_full = bars + 10;
+  uint64_t* done = bars + 11;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 13);
+  if (tid == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(q_full + s, 32);
+      mbar_init(g_full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 2 * kTile);
+    mbar_init(ds_full, 2 * kTile);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ---- TMA: K and V, then Q and dO tile by tile with lse and delta ----
+    int issued = 0;
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
+      load_tile<D>(smem + L::kAOff, mk, kv_full, k0, hk, b);
+      load_tile<D>(smem + L::kBOff, mv, kv_full, k0, hk, b);
+    }
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      const int st = i & 1, h = hk * group + i / per, q0 = (first + i % per) * kTile;
+      if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait(empty + st, ((i >> 1) - 1) & 1,
+                                                         abort_flag, a.status));
+      if (!ok) break;
+      const long at = ((long)b * pb.H + h) * pb.Nq;
+      for (int x = lane; x < kTile; x += 32) {
+        // a row outside the tensor or without keys: exp(S - inf) = 0
+        const int row = q0 + x;
+        const bool live = row < pb.Nq && dense_visible(pb, len, row) > 0;
+        rows[st * 256 + x] = live ? __ldg(a.lse + at + row) * kLog2e : INFINITY;
+        rows[st * 256 + kTile + x] = live ? __ldg(a.delta + at + row) : 0.f;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full + st, L::kTileBytes);
+        load_tile<D>(smem + L::kXOff + st * L::kTileBytes, mq, q_full + st, q0, h, b);
+        mbar_arrive_expect_tx(g_full + st, L::kTileBytes);
+        load_tile<D>(smem + L::kYOff + st * L::kTileBytes, mg, g_full + st, q0, h, b);
+      } else {
+        mbar_arrive(q_full + st);
+      }
+      issued = i + 1;
+    }
+    if (lane == 0 && n > 0 && *abort_flag) {  // wait (bounded) for the loads in flight
+      drain_bar(kv_full, 0);
+      for (int s = 0; s < L::kStages; ++s)
+        if (issued > s) {
+          drain_bar(q_full + s, ((issued - 1 - s) >> 1) & 1);
+          drain_bar(g_full + s, ((issued - 1 - s) >> 1) & 1);
+        }
+    }
+  } else if (warp == 9) {
+    // ---- MMA issue ----
+    if (lane == 0 && n > 0) {
+      const uint64_t dk = desc_kmajor(smem_u32(smem + L::kAOff));
+      const uint64_t dv = desc_kmajor(smem_u32(smem + L::kBOff));
+      const uint32_t sx = smem_u32(smem + L::kXOff), sy = smem_u32(smem + L::kYOff);
+      bool ok = mbar_wait(kv_full, 0, abort_flag, a.status) &&
+                mbar_wait(q_full, 0, abort_flag, a.status);
+      if (ok) {
+        mma_nt<D>(tmem, dk, desc_kmajor(sx));
+        mma_commit(s_full);
+        ok = mbar_wait(g_full, 0, abort_flag, a.status);
+      }
+      if (ok) {
+        mma_nt<D>(tmem + L::kDPCol, dv, desc_kmajor(sy));
+        mma_commit(dp_full);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t x = sx + (i & 1) * L::kTileBytes, y = sy + (i & 1) * L::kTileBytes;
+        const uint32_t x1 = sx + (~i & 1) * L::kTileBytes, y1 = sy + (~i & 1) * L::kTileBytes;
+        const uint32_t ph1 = ((i + 1) >> 1) & 1;
+        if (!(ok = mbar_wait(p_full, i & 1, abort_flag, a.status))) break;
+        tc_fence_after();
+        mma_halves<D>(tmem + L::kAccCol, tmem, desc_mnmajor(y, kChunk), i > 0);
+        if (i + 1 < n) {  // (in order: over P once dV has read it)
+          if (!(ok = mbar_wait(q_full + (~i & 1), ph1, abort_flag, a.status))) break;
+          mma_nt<D>(tmem, dk, desc_kmajor(x1));
+          mma_commit(s_full);
+        }
+        if (!(ok = mbar_wait(ds_full, i & 1, abort_flag, a.status))) break;
+        tc_fence_after();
+        mma_halves<D>(tmem + L::kAccCol + D, tmem + L::kDPCol, desc_mnmajor(x, kChunk), i > 0);
+        mma_commit(empty + (i & 1));
+        if (i + 1 < n) {
+          if (!(ok = mbar_wait(g_full + (~i & 1), ph1, abort_flag, a.status))) break;
+          mma_nt<D>(tmem + L::kDPCol, dv, desc_kmajor(y1));
+          mma_commit(dp_full);
+        }
+      }
+      mma_commit(done);
+      if (*abort_flag) drain_bar(done, 0);
+    }
+  } else {
+    // ---- thread = key r, 64 query columns ----
+    const int half = warp >> 2, r = tid & (kTile - 1), key = k0 + r;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + half * 64, tp = ts + L::kDPCol;
+    const float sl = pb.scale * kLog2e;
+    const float2 sl2 = make_float2(sl, sl);
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1, q0 = (first + i % per) * kTile;
+      const float* lse2 = rows + st * 256 + half * 64;
+      const float* delta = lse2 + kTile;
+      if (!(ok = mbar_wait(q_full + st, (i >> 1) & 1, abort_flag, a.status))) break;
+      if (!(ok = mbar_wait(s_full, i & 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      float p[64];
+      load_half(ts, p);
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(lse2 + e);
+        const float2 u = fma2(make_float2(p[e], p[e + 1]), sl2, make_float2(-l.x, -l.y));
+        const float2 w = fma2(make_float2(p[e + 2], p[e + 3]), sl2, make_float2(-l.z, -l.w));
+        p[e] = ex2(u.x);
+        p[e + 1] = ex2(u.y);
+        p[e + 2] = ex2(w.x);
+        p[e + 3] = ex2(w.y);
+      }
+      // the first column whose query sees this key
+      const int lo = (key >= len ? kTile : pb.causal ? key - shift - q0 : 0) - half * 64;
+      const bool masked = k0 + kTile > len || (pb.causal && k0 + kTile - 1 > q0 + shift);
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e < lo) p[e] = 0.f;
+      }
+      store_half(ts, p);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full);
+      if (!(ok = mbar_wait(dp_full, i & 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      float d[64];
+      load_half(tp, d);
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(delta + e);
+        d[e] = p[e] * (d[e] - l.x);
+        d[e + 1] = p[e + 1] * (d[e + 1] - l.y);
+        d[e + 2] = p[e + 2] * (d[e + 2] - l.z);
+        d[e + 3] = p[e + 3] * (d[e + 3] - l.w);
+      }
+      if (masked) {  // what lies past the length may be NaN: selected away, not multiplied
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e < lo) d[e] = 0.f;
+      }
+      store_half(tp, d);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
+    tc_fence_after();
+    // dV (warps 0-3) and dK (warps 4-7) through the tiles of K and V; a tile
+    // that no query sees gets zeros
+    uint8_t* so = smem + (half ? L::kBOff : L::kAOff);
+    if (ok) {
+      accumulator_row<D>(so, r, tmem + lane_off + L::kAccCol + half * D, half ? pb.scale : 1.f,
+                         n > 0);
+      fence_proxy_async_smem();
+    }
+    named_barrier(1 + half, kTile);
+    if (r == 0 && ok && !*abort_flag) {
+      for (int c = 0; c < L::kCh; ++c)
+        if (c * 64 < pb.d)
+          tma_store_4d(half ? &mdk.map : &mdv.map, so + c * kChunk, c * 64, k0, hk, b);
+      bulk_commit();
+      bulk_wait_read<0>();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// dQ of 128 queries of a head: dQ = scale sum over the key tiles of dS K,
+// dS = P (dO V^T - delta).  P stays in registers, so the next S starts as soon
+// as this one is read, and runs beside its exponentials.
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    dense_dq_tc_kernel(const __grid_constant__ TileMap mq, const __grid_constant__ TileMap mk,
+                       const __grid_constant__ TileMap mv, const __grid_constant__ TileMap mg,
+                       const __grid_constant__ TileMap mdq, const __grid_constant__ BwdArgs a) {
+  using L = BwdLayout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) atomicExch(a.status, 2);
+    return;
+  }
+  const DenseProblem& pb = a.pb;
+  const int heads = pb.B * pb.H;
+  const int tile = pb.causal ? a.tiles - 1 - blockIdx.x / heads : blockIdx.x % a.tiles;
+  const int bh = pb.causal ? blockIdx.x % heads : blockIdx.x / a.tiles;
+  const int h = bh % pb.H, b = bh / pb.H, hk = h / (pb.H / pb.Hkv);
+  const int q0 = tile * kTile;
+  const int len = dense_len(pb, b);
+  const int n = (dense_visible(pb, len, min(q0 + kTile, pb.Nq) - 1) + kTile - 1) / kTile;
+  const int tail = n * kTile > len && len < pb.Nk ? len - (n - 1) * kTile : kTile;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* qg_full = bars;
+  uint64_t* k_full = bars + 1;   // [stages]
+  uint64_t* v_full = bars + 3;
+  uint64_t* k_empty = bars + 5;
+  uint64_t* v_empty = bars + 7;
+  uint64_t* k_tail = bars + 9;
+  uint64_t* s_full = bars + 10;
+  uint64_t* s_read = bars + 11;
+  uint64_t* dp_full = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* done = bars + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 16);
+  if (tid == 0) {
+    mbar_init(qg_full, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(k_full + s, 1);
+      mbar_init(v_full + s, 1);
+      mbar_init(k_empty + s, 1);
+      mbar_init(v_empty + s, 1);
+    }
+    mbar_init(k_tail, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_read, 2 * kTile);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 2 * kTile);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ---- TMA: Q and dO, then K and V tile by tile ----
+    bool ok = true;
+    int kt = 0, vt = 0;
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(qg_full, 2 * L::kTileBytes);
+      load_tile<D>(smem + L::kAOff, mq, qg_full, q0, h, b);
+      load_tile<D>(smem + L::kBOff, mg, qg_full, q0, h, b);
+      for (int j = 0; j < n; ++j) {
+        const int st = j & 1;
+        const uint32_t par = ((j >> 1) - 1) & 1;
+        if (j >= 2 && !(ok = mbar_wait(k_empty + st, par, abort_flag, a.status))) break;
+        mbar_arrive_expect_tx(k_full + st, L::kTileBytes);
+        load_tile<D>(smem + L::kXOff + st * L::kTileBytes, mk, k_full + st, j * kTile, hk, b);
+        kt = j + 1;
+        if (j >= 2 && !(ok = mbar_wait(v_empty + st, par, abort_flag, a.status))) break;
+        mbar_arrive_expect_tx(v_full + st, L::kTileBytes);
+        load_tile<D>(smem + L::kYOff + st * L::kTileBytes, mv, v_full + st, j * kTile, hk, b);
+        vt = j + 1;
+      }
+    }
+    __syncwarp();
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok && n > 0 && tail < kTile) {
+      // keys past the length may hold anything (0 x NaN): zeros in their place
+      const int st = (n - 1) & 1;
+      if (mbar_wait(k_full + st, ((n - 1) >> 1) & 1, abort_flag, a.status)) {
+        uint8_t* sk = smem + L::kXOff + st * L::kTileBytes;
+        for (int x = lane; x < (kTile - tail) * L::kCh * 8; x += 32)
+          *row_unit(sk, tail + x / (L::kCh * 8), x % (L::kCh * 8)) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_tail);
+      }
+    }
+    if (lane == 0 && n > 0 && *abort_flag) {
+      drain_bar(qg_full, 0);
+      for (int s = 0; s < L::kStages; ++s) {
+        if (kt > s) drain_bar(k_full + s, ((kt - 1 - s) >> 1) & 1);
+        if (vt > s) drain_bar(v_full + s, ((vt - 1 - s) >> 1) & 1);
+      }
+    }
+  } else if (warp == 9) {
+    // ---- MMA issue ----
+    if (lane == 0 && n > 0) {
+      const uint64_t dq = desc_kmajor(smem_u32(smem + L::kAOff));
+      const uint64_t dg = desc_kmajor(smem_u32(smem + L::kBOff));
+      const uint32_t sx = smem_u32(smem + L::kXOff), sy = smem_u32(smem + L::kYOff);
+      auto key_tile = [&](int j) {
+        return mbar_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag, a.status) &&
+               (j + 1 < n || tail == kTile || mbar_wait(k_tail, 0, abort_flag, a.status));
+      };
+      bool ok = mbar_wait(qg_full, 0, abort_flag, a.status) && key_tile(0);
+      if (ok) {
+        mma_nt<D>(tmem, dq, desc_kmajor(sx));
+        mma_commit(s_full);
+        ok = mbar_wait(v_full, 0, abort_flag, a.status);
+      }
+      if (ok) {
+        mma_nt<D>(tmem + L::kDPCol, dg, desc_kmajor(sy));
+        mma_commit(dp_full);
+        mma_commit(v_empty);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int st = j & 1, s1 = st ^ 1;
+        if (j + 1 < n) {
+          if (!(ok = key_tile(j + 1) && mbar_wait(s_read, j & 1, abort_flag, a.status))) break;
+          tc_fence_after();
+          mma_nt<D>(tmem, dq, desc_kmajor(sx + s1 * L::kTileBytes));
+          mma_commit(s_full);
+        }
+        if (!(ok = mbar_wait(ds_full, j & 1, abort_flag, a.status))) break;
+        tc_fence_after();
+        mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol,
+                      desc_mnmajor(sx + st * L::kTileBytes, kChunk), j > 0);
+        mma_commit(k_empty + st);
+        if (j + 1 < n) {  // (in order: over dS once dQ has read it)
+          if (!(ok = mbar_wait(v_full + s1, ((j + 1) >> 1) & 1, abort_flag, a.status))) break;
+          mma_nt<D>(tmem + L::kDPCol, dg, desc_kmajor(sy + s1 * L::kTileBytes));
+          mma_commit(dp_full);
+          mma_commit(v_empty + s1);
+        }
+      }
+      mma_commit(done);
+      if (*abort_flag) drain_bar(done, 0);
+    }
+  } else {
+    // ---- thread = query r, 64 key columns ----
+    const int half = warp >> 2, r = tid & (kTile - 1), row = q0 + r;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_off + half * 64, tp = ts + L::kDPCol;
+    const int vis = dense_visible(pb, len, row), all = dense_visible(pb, len, q0);
+    const long at = ((long)b * pb.H + h) * pb.Nq + row;
+    const bool live = row < pb.Nq && vis > 0;
+    const float lse2 = live ? __ldg(a.lse + at) * kLog2e : INFINITY;
+    const float delta = live ? __ldg(a.delta + at) : 0.f;
+    const float sl = pb.scale * kLog2e;
+    const float2 sl2 = make_float2(sl, sl), base2 = make_float2(-lse2, -lse2);
+    const float2 nd2 = make_float2(-delta, -delta);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = mbar_wait(s_full, j & 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      float p[64];
+      load_half(ts, p);
+      tc_fence_before();
+      mbar_arrive(s_read);
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        const float2 u = fma2(make_float2(p[e], p[e + 1]), sl2, base2);
+        p[e] = ex2(u.x);
+        p[e + 1] = ex2(u.y);
+      }
+      if (!(ok = mbar_wait(dp_full, j & 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      float d[64];
+      load_half(tp, d);
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        const float2 u = mul2(make_float2(p[e], p[e + 1]),
+                              add2(make_float2(d[e], d[e + 1]), nd2));
+        d[e] = u.x;
+        d[e + 1] = u.y;
+      }
+      if ((j + 1) * kTile > all) {  // hidden keys, whatever the products hold
+        const int lim = vis - j * kTile - half * 64;
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= lim) d[e] = 0.f;
+      }
+      store_half(tp, d);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
+    tc_fence_after();
+    if (half == 0) {
+      uint8_t* so = smem + L::kAOff;
+      if (ok) {
+        accumulator_row<D>(so, r, tmem + lane_off + L::kAccCol, pb.scale, n > 0);
+        fence_proxy_async_smem();
+      }
+      named_barrier(1, kTile);
+      if (r == 0 && ok && !*abort_flag) {
+        for (int c = 0; c < L::kCh; ++c)
+          if (c * 64 < pb.d) tma_store_4d(&mdq.map, so + c * kChunk, c * 64, q0, h, b);
+        bulk_commit();
+        bulk_wait_read<0>();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -441,6 +991,31 @@ cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, c
   });
 }
 
+template <int D>
+cudaError_t backward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mg,
+                       const TileMap& mdq, const TileMap& mdk, const TileMap& mdv, BwdArgs a,
+                       cudaStream_t stream, int* launches) {
+  using L = BwdLayout<D>;
+  cudaError_t e = cudaFuncSetAttribute(dense_dkv_tc_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  a.tiles = (a.pb.Nk + kTile - 1) / kTile;
+  e = timed_launch("dense_dkv_tc", stream, launches, [&] {
+    dense_dkv_tc_kernel<D><<<(unsigned)a.tiles * a.pb.Hkv * a.pb.B, kBwdThreads, L::kBytes,
+                             stream>>>(mq, mk, mv, mg, mdk, mdv, a);
+  });
+  if (e != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(dense_dq_tc_kernel<D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes)) !=
+      cudaSuccess)
+    return e;
+  a.tiles = (a.pb.Nq + kTile - 1) / kTile;
+  return timed_launch("dense_dq_tc", stream, launches, [&] {
+    dense_dq_tc_kernel<D><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
+                            stream>>>(mq, mk, mv, mg, mdq, a);
+  });
+}
+
 }  // namespace
 
 bool dense_tc_rows(const void* p, const HeadStrides& s, int N, int d) {
@@ -462,6 +1037,27 @@ cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* 
   const FwdArgs a = {lse, pb, (pb.Nq + 2 * kTile - 1) / (2 * kTile), status};
   return pb.d <= 64 ? forward_d<64>(mq, mk, mv, mo, a, stream, launches)
                     : forward_d<128>(mq, mk, mv, mo, a, stream, launches);
+}
+
+cudaError_t dense_tc_backward(const bf16* q, const bf16* k, const bf16* v, const bf16* out,
+                              const float* lse, const bf16* dout, bf16* dq, bf16* dk, bf16* dv,
+                              float* delta, const DenseProblem& pb, int* status,
+                              cudaStream_t stream, int* launches) {
+  TileMap mq, mk, mv, mg, mdq, mdk, mdv;
+  if (!make_tile_map(&mq, q, pb.q, pb.B, pb.H, pb.Nq, pb.d) ||
+      !make_tile_map(&mk, k, pb.k, pb.B, pb.Hkv, pb.Nk, pb.d) ||
+      !make_tile_map(&mv, v, pb.v, pb.B, pb.Hkv, pb.Nk, pb.d) ||
+      !make_tile_map(&mg, dout, pb.dout, pb.B, pb.H, pb.Nq, pb.d) ||
+      !make_tile_map(&mdq, dq, pb.dq, pb.B, pb.H, pb.Nq, pb.d) ||
+      !make_tile_map(&mdk, dk, pb.dk, pb.B, pb.Hkv, pb.Nk, pb.d) ||
+      !make_tile_map(&mdv, dv, pb.dv, pb.B, pb.Hkv, pb.Nk, pb.d))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = dense_delta<bf16>(out, dout, delta, pb, stream, launches);
+  if (e != cudaSuccess) return e;
+  const BwdArgs a = {lse, delta, pb, 0, status};
+  return pb.d <= 64
+             ? backward_d<64>(mq, mk, mv, mg, mdq, mdk, mdv, a, stream, launches)
+             : backward_d<128>(mq, mk, mv, mg, mdq, mdk, mdv, a, stream, launches);
 }
 
 }  // namespace monarch
