@@ -2,10 +2,12 @@
 //
 // The cache of a sequence is a list of pages; key j sits in row j % page_size
 // of page table[b][j / page_size].  The keys are cut into chunks that CTAs
-// take independently, each for all query heads that share its key/value head
+// take independently, each for the query heads that share its key/value head
 // (so the cache is read once); a chunk gives its own maximum, sum and
 // unnormalised output, and a second launch joins the chunks in order (no
-// atomics).  Bound: the bytes of the cache.
+// atomics).  One pass: every warp walks its tiles of a chunk under a running
+// maximum, and the four warps of the CTA are joined in shared memory.
+// Bound: the bytes of the cache.
 #include "dense.cuh"
 
 #include <math.h>
@@ -13,6 +15,7 @@
 #include <algorithm>
 
 #include "launch.cuh"
+#include "tc_ptx.cuh"
 #include "timing.cuh"
 
 namespace monarch {
@@ -20,218 +23,637 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 128;
-constexpr int kTile = 32;       // keys per tile
-constexpr int kHeads = 8;       // query heads per CTA
-constexpr int kBadIndex = MONARCH_DEVICE_BAD_INDEX_FLAG;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRows = 16;  // query heads of a CTA on the tensor cores (M of the product)
 
 struct Split {
   int chunk;   // keys per chunk
   int chunks;  // chunks of the longest sequence that the table allows
-  int hg;      // groups of kHeads query heads per key/value head
 };
 
+// Four waves of two CTAs per SM over the longest sequences (ragged lengths
+// leave some empty), and 128 keys a chunk at least: fewer do not fill the
+// loads in flight of a CTA, and each chunk's result is read again by the join.
 Split make_split(const DecodeProblem& pb) {
-  Split s;
   const long top = (long)pb.max_pages * pb.page_size;
-  s.hg = (pb.H / pb.Hkv + kHeads - 1) / kHeads;
-  const long units = (long)pb.B * pb.Hkv * s.hg;
-  // about eight CTAs per SM in all, at least 128 keys each
-  long n = std::max(1L, std::min((top + 127) / 128, 8L * num_sms() / std::max(1L, units)));
-  s.chunk = (int)(((top + n - 1) / n + kTile - 1) / kTile * kTile);
-  s.chunk = std::max(s.chunk, kTile);
+  const long units = (long)pb.B * pb.Hkv * ((pb.H / pb.Hkv + kRows - 1) / kRows);
+  const long n = std::max(1L, std::min((top + 127) / 128, 8L * num_sms() / units));
+  Split s;
+  s.chunk = (int)(((top + n - 1) / n + 127) / 128 * 128);
+  s.chunk = std::max(s.chunk, 128);
   s.chunks = (int)std::max(1L, (top + s.chunk - 1) / s.chunk);
   return s;
 }
 
-__device__ __forceinline__ int seq_len(const DecodeProblem& pb, int b, int* status) {
-  const int n = __ldg(pb.lens + b);
-  const int top = pb.max_pages * pb.page_size;
-  if (n < 0 || n > top) {
-    atomicCAS(status, 0, kBadIndex);
-    return min(max(n, 0), top);
-  }
-  return n;
+struct Parts {
+  float2* ml;  // [chunk][b][h]: maximum in log2 units, sum
+  float* o;    // [chunk][b][h][d], unnormalised
+};
+
+// One CTA's share: heads [h0, h0 + nh) of sequence b over keys [j0, j1).
+struct Share {
+  int b, hk, h0, nh, c, j0, j1;
+};
+
+__device__ __forceinline__ Share share_of(const DecodeProblem& pb, const Split& sp, int heads,
+                                          int* status) {
+  const int group = pb.H / pb.Hkv, hgs = (group + heads - 1) / heads;
+  Share s;
+  int x = blockIdx.x;
+  s.c = x % sp.chunks;
+  x /= sp.chunks;
+  const int hg = x % hgs;
+  x /= hgs;
+  s.hk = x % pb.Hkv;
+  s.b = x / pb.Hkv;
+  s.h0 = s.hk * group + hg * heads;
+  s.nh = min(heads, (s.hk + 1) * group - s.h0);
+  const int n = __ldg(pb.lens + s.b), top = pb.max_pages * pb.page_size;
+  if (n < 0 || n > top) atomicCAS(status, 0, MONARCH_DEVICE_BAD_INDEX_FLAG);
+  s.j0 = s.c * sp.chunk;
+  s.j1 = min(min(max(n, 0), top), s.j0 + sp.chunk);
+  return s;
 }
 
-// Partial results: [chunk][b][h] of (maximum in log2 units, sum), then
-// [chunk][b][h][d] of unnormalised outputs.
-template <typename T, int DP>
+// Page and row of key j, page -1 where there is none or it lies outside the
+// cache (which is recorded).
+__device__ __forceinline__ int2 place(const DecodeProblem& pb, const Share& s, int j,
+                                      int* status) {
+  if (j >= s.j1) return make_int2(-1, 0);
+  const int p = j / pb.page_size;
+  int page = __ldg(pb.table + (long)s.b * pb.max_pages + p);
+  if (page < 0 || page >= pb.n_pages) {
+    atomicCAS(status, 0, MONARCH_DEVICE_BAD_INDEX_FLAG);
+    page = -1;
+  }
+  return make_int2(page, j - p * pb.page_size);
+}
+
+// The four warps' results (m, z per head and o[head][channel], in shared
+// memory, warps `o_step` floats apart) joined and written: as a part, or as
+// the result itself where one chunk holds every sequence.
+template <typename T>
+__device__ __forceinline__ void join_warps(const float (*m)[kRows], const float (*z)[kRows],
+                                           const float* o, int o_step, int pitch,
+                                           const DecodeProblem& pb, const Split& sp,
+                                           const Share& s, Parts part, T* out, float* lse) {
+  const long row0 = (long)s.b * pb.H + s.h0;
+  for (int x = threadIdx.x; x < s.nh * pb.d; x += kThreads) {
+    const int h = x / pb.d, e = x % pb.d;
+    float mm = m[0][h];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, m[w][h]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float zz = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(m[w][h] - base);
+      zz = fmaf(z[w][h], f, zz);
+      acc = fmaf(o[w * o_step + h * pitch + e], f, acc);
+    }
+    if (sp.chunks == 1) {
+      out[s.b * pb.out_b + (s.h0 + h) * pb.out_h + e] = from_f32<T>(acc / zz);
+      if (e == 0) lse[row0 + h] = (mm + log2f(zz)) * kLn2;
+    } else {
+      const long at = (long)s.c * pb.B * pb.H + row0 + h;
+      part.o[at * pb.d + e] = acc;
+      if (e == 0) part.ml[at] = make_float2(mm, zz);
+    }
+  }
+}
+
+// An empty sequence's only chunk.
+template <typename T>
+__device__ __forceinline__ void write_empty(const DecodeProblem& pb, const Share& s, T* out,
+                                            float* lse) {
+  for (int x = threadIdx.x; x < s.nh * pb.d; x += kThreads) {
+    const int h = x / pb.d, e = x % pb.d;
+    out[s.b * pb.out_b + (s.h0 + h) * pb.out_h + e] = from_f32<T>(0.f);
+    if (e == 0) lse[(long)s.b * pb.H + s.h0 + h] = -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bf16 rows of 16-byte alignment, d a multiple of 8 up to 128: 16 heads by 8
+// keys products (the heads padded to 16 rows; the tensor cores have room to
+// spare beside the loads).  Each warp streams its own tiles of 16 (d > 64) or
+// 32 keys through three 8 KB slots by 16-byte asynchronous copies, without
+// any barrier between the warps.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DP>
+struct MmaTile {
+  static constexpr int kKeys = 2048 / DP, kUnits = DP / 8;  // 16-byte units of a row
+  static constexpr int kHalf = kKeys * DP * 2;              // bytes of K (or V) of a tile
+  static constexpr int kStages = 3, kWarpBytes = kStages * 2 * kHalf;
+  static constexpr int kPitch = DP + 4;
+  static_assert(kRows * kPitch * 4 <= kWarpBytes, "the result reuses the warp's slots");
+};
+
+template <int DP>
 __global__ void __launch_bounds__(kThreads)
-    decode_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
-                  float2* __restrict__ part_ml, float* __restrict__ part_o, DecodeProblem pb,
-                  Split sp, int* status) {
-  constexpr int kPitch = DP + 4, kCols = (DP + kThreads - 1) / kThreads;
-  extern __shared__ __align__(16) float smf[];
-  float* sQ = smf;                     // [kHeads][DP]
-  float* sK = sQ + kHeads * DP;        // [kTile][kPitch]
-  float* sV = sK + kTile * kPitch;
-  float* sP = sV + kTile * kPitch;     // [kHeads][kTile]
-  __shared__ float sM[kHeads], sZ[kHeads], sC[kHeads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int x = blockIdx.x;
-  const int c = x % sp.chunks;
-  x /= sp.chunks;
-  const int hg = x % sp.hg;
-  x /= sp.hg;
-  const int hk = x % pb.Hkv, b = x / pb.Hkv;
-  const int group = pb.H / pb.Hkv;
-  const int h0 = hk * group + hg * kHeads;
-  const int nh = min(kHeads, (hk + 1) * group - h0);
-  const int len = seq_len(pb, b, status);
-  const int j0 = c * sp.chunk, j1 = min(len, j0 + sp.chunk);
-  if (j0 >= j1) return;  // the join reads no chunk from the length on
-  for (int i = tid; i < kHeads * DP; i += kThreads) {
-    const int h = i / DP, e = i % DP;
-    sQ[i] = h < nh && e < pb.d ? to_f32(q[b * pb.q_b + (h0 + h) * pb.q_h + e]) : 0.f;
+    decode_mma_kernel(const bf16* __restrict__ q, const bf16* __restrict__ kc,
+                      const bf16* __restrict__ vc, Parts part, bf16* __restrict__ out,
+                      float* __restrict__ lse, DecodeProblem pb, Split sp, int* status) {
+  using L = MmaTile<DP>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sm[kWarps][kRows], sz[kWarps][kRows];
+  tc::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Share s = share_of(pb, sp, kRows, status);
+  if (s.j0 >= s.j1) {  // the join reads no chunk from the length on
+    if (sp.chunks == 1) write_empty(pb, s, out, lse);
+    return;
   }
-  if (tid < kHeads) {
-    sM[tid] = -INFINITY;
-    sZ[tid] = 0.f;
+  uint8_t* ring = smem + warp * L::kWarpBytes;
+  const uint32_t ring32 = tc::smem_u32(ring);
+  const int g = lane >> 2, t4 = lane & 3;
+  // Q as A operands: rows g and g + 8 (heads), channels 16 kk + 2 t4 and + 8
+  uint32_t qa[DP / 16][4];
+  {
+    const bf16* q0 = q + s.b * pb.q_b + s.h0 * pb.q_h;
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int h = g + (x & 1) * 8, e = kk * 16 + (x >> 1) * 8 + t4 * 2;
+        qa[kk][x] = h < s.nh && e < pb.d
+                        ? __ldg(reinterpret_cast<const unsigned int*>(q0 + h * pb.q_h + e))
+                        : 0u;
+      }
   }
-  float o[kCols][kHeads];
+  const int n = max(0, ((s.j1 - s.j0 + L::kKeys - 1) / L::kKeys - warp + kWarps - 1) / kWarps);
+  auto tile_key = [&](int i) { return s.j0 + (warp + i * kWarps) * L::kKeys; };
+  auto lookup = [&](int i) {  // lane = key
+    return i < n ? place(pb, s, tile_key(i) + (lane & (L::kKeys - 1)), status)
+                 : make_int2(-1, 0);
+  };
+  auto fetch = [&](int i, int2 at) {
+    if (i < n) {
+      const uint32_t dst = ring32 + (i % L::kStages) * 2 * L::kHalf;
+      const bf16 *k0 = kc + s.hk * pb.k_h, *v0 = vc + s.hk * pb.v_h;
 #pragma unroll
-  for (int i = 0; i < kCols; ++i)
+      for (int x = 0; x < L::kKeys * L::kUnits / 32; ++x) {
+        const int r = (x * 32 + lane) / L::kUnits, u = lane % L::kUnits;
+        const int page = __shfl_sync(0xffffffffu, at.x, r), row = __shfl_sync(0xffffffffu, at.y, r);
+        const bool there = page >= 0 && u * 8 < pb.d;
+        const bf16* ks = there ? k0 + page * pb.k_page + row * pb.k_n + u * 8 : kc;
+        const bf16* vs = there ? v0 + page * pb.v_page + row * pb.v_n + u * 8 : vc;
+        const uint32_t o = dst + r * DP * 2 + ((u ^ (r & 7)) << 4);
+        copy16(o, ks, there);
+        copy16(o + L::kHalf, vs, there);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float o[DP / 8][4];
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) o[i][h] = 0.f;
+  for (int x = 0; x < DP / 8; ++x)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f;  // heads g and g + 8
   const float sl = pb.scale * kLog2e;
-  for (int t0 = j0; t0 < j1; t0 += kTile) {
-    __syncthreads();
-    for (int i = tid; i < kTile * DP; i += kThreads) {
-      const int r = i / DP, e = i % DP, j = t0 + r;
-      float kv = 0.f, vv = 0.f;
-      if (j < j1 && e < pb.d) {
-        const int page = __ldg(pb.table + (long)b * pb.max_pages + j / pb.page_size);
-        if (page >= 0 && page < pb.n_pages) {
-          kv = to_f32(kc[page * pb.k_page + hk * pb.k_h + (j % pb.page_size) * pb.k_n + e]);
-          vv = to_f32(vc[page * pb.v_page + hk * pb.v_h + (j % pb.page_size) * pb.v_n + e]);
+#pragma unroll
+  for (int i = 0; i < L::kStages - 1; ++i) fetch(i, lookup(i));
+  int2 next = lookup(L::kStages - 1);
+  for (int i = 0; i < n; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 2) : "memory");
+    __syncwarp();  // tile i is there for every lane, and tile i - 1 is read
+    fetch(i + L::kStages - 1, next);
+    next = lookup(i + L::kStages);
+    const uint32_t sk = ring32 + (i % L::kStages) * 2 * L::kHalf, sv = sk + L::kHalf;
+    const int left = s.j1 - tile_key(i);
+    float c[L::kKeys / 8][4];
+#pragma unroll
+    for (int x = 0; x < L::kKeys / 8; ++x) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) c[x][y] = 0.f;
+      const int r = x * 8 + (lane & 7);
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; kk += 2) {  // four 8-channel blocks of 8 keys
+        uint32_t kb[4];
+        ldsm4(kb, sk + r * DP * 2 + (((kk * 2 + (lane >> 3)) ^ (r & 7)) << 4));
+        mma16816(c[x], qa[kk], kb[0], kb[1]);
+        mma16816(c[x], qa[kk + 1], kb[2], kb[3]);
+      }
+    }
+    float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < L::kKeys / 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const bool see = x * 8 + t4 * 2 + y < left;
+        c[x][y] = see ? c[x][y] * sl : -INFINITY;
+        c[x][2 + y] = see ? c[x][2 + y] * sl : -INFINITY;
+        a0 = fmaxf(a0, c[x][y]);
+        a1 = fmaxf(a1, c[x][2 + y]);
+      }
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+      a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, x));
+      a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, x));
+    }
+    if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
+      const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+      const float f0 = m0 == n0 ? 1.f : exp2f(m0 - n0), f1 = m1 == n1 ? 1.f : exp2f(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      z0 *= f0;
+      z1 *= f1;
+#pragma unroll
+      for (int x = 0; x < DP / 8; ++x) {
+        o[x][0] *= f0;
+        o[x][1] *= f0;
+        o[x][2] *= f1;
+        o[x][3] *= f1;
+      }
+    }
+    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+    for (int kk = 0; kk < L::kKeys / 16; ++kk) {
+      uint32_t pa[4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float* cc = c[kk * 2 + x];
+        const float p0 = tc::ex2(cc[0] - b0), p1 = tc::ex2(cc[1] - b0);
+        const float p2 = tc::ex2(cc[2] - b1), p3 = tc::ex2(cc[3] - b1);
+        z0 += p0 + p1;
+        z1 += p2 + p3;
+        pa[2 * x] = tc::pack_bf16x2(p0, p1);
+        pa[2 * x + 1] = tc::pack_bf16x2(p2, p3);
+      }
+      const int r = kk * 16 + (lane & 15);
+#pragma unroll
+      for (int x = 0; x < DP / 8; x += 2) {  // 16 keys by two 8-channel blocks
+        uint32_t vb[4];
+        ldsm4_trans(vb, sv + r * DP * 2 + (((x + (lane >> 4)) ^ (r & 7)) << 4));
+        mma16816(o[x], pa, vb[0], vb[1]);
+        mma16816(o[x + 1], pa, vb[2], vb[3]);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int x = 1; x < 4; x <<= 1) {
+    z0 += __shfl_xor_sync(0xffffffffu, z0, x);
+    z1 += __shfl_xor_sync(0xffffffffu, z1, x);
+  }
+  if (t4 == 0) {
+    sm[warp][g] = m0;
+    sm[warp][g + 8] = m1;
+    sz[warp][g] = z0;
+    sz[warp][g + 8] = z1;
+  }
+  float* so = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int x = 0; x < DP / 8; ++x) {
+    const int e = x * 8 + t4 * 2;
+    *reinterpret_cast<float2*>(so + g * L::kPitch + e) = make_float2(o[x][0], o[x][1]);
+    *reinterpret_cast<float2*>(so + (g + 8) * L::kPitch + e) = make_float2(o[x][2], o[x][3]);
+  }
+  __syncthreads();
+  join_warps<bf16>(sm, sz, reinterpret_cast<const float*>(smem), L::kWarpBytes / 4, L::kPitch, pb,
+                   sp, s, part, out, lse);
+}
+
+// ---------------------------------------------------------------------------
+// Every other case, in fp32 on the CUDA cores: a lane holds CH = DP / 32
+// channels of a row, GH heads and KT keys at a time.  The KT x GH dot
+// products are summed over the lanes by halving (each step leaves a lane half
+// of the values it had), about one shuffle a product.
+// ---------------------------------------------------------------------------
+template <typename T, int CH>
+__device__ __forceinline__ void load_channels(float (&x)[CH], const T* p, int e, int d, bool vec) {
+  if (vec) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < CH; i += 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(p + e + i));
+        x[i] = v.x;
+        x[i + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; i += 2) {
+        const uint32_t v = __ldg(reinterpret_cast<const unsigned int*>(p + e + i));
+        x[i] = __uint_as_float(v << 16);
+        x[i + 1] = __uint_as_float(v & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) x[i] = e + i < d ? to_f32(p[e + i]) : 0.f;
+  }
+}
+
+template <typename T, int CH>
+__device__ __forceinline__ void load_vector(float (&x)[CH], const T* p) {
+  if constexpr (sizeof(T) == 4 && CH >= 4) {
+#pragma unroll
+    for (int i = 0; i < CH; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      x[i] = v.x;
+      x[i + 1] = v.y;
+      x[i + 2] = v.z;
+      x[i + 3] = v.w;
+    }
+  } else {
+    load_channels<T, CH>(x, p, 0, CH, true);
+  }
+}
+
+template <typename T, int DP, int GH, int KT>
+__global__ void __launch_bounds__(kThreads)
+    decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc,
+                       const T* __restrict__ vc, Parts part, T* __restrict__ out,
+                       float* __restrict__ lse, DecodeProblem pb, Split sp, bool vec,
+                       int* status) {
+  constexpr int CH = DP / 32, kVals = KT * GH;
+  static_assert(kVals <= 32 && (kVals & (kVals - 1)) == 0, "dot products of a tile");
+  __shared__ float sm[kWarps][kRows], sz[kWarps][kRows];
+  __shared__ float so[kWarps][GH][DP + 4];
+  tc::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * CH;
+  const Share s = share_of(pb, sp, GH, status);
+  if (s.j0 >= s.j1) {
+    if (sp.chunks == 1) write_empty(pb, s, out, lse);
+    return;
+  }
+  const float sl = pb.scale * kLog2e;
+  float qr[GH][CH], o[GH][CH], m[GH], z[GH];
+#pragma unroll
+  for (int h = 0; h < GH; ++h) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      qr[h][i] = h < s.nh && e0 + i < pb.d
+                     ? to_f32(q[s.b * pb.q_b + (s.h0 + h) * pb.q_h + e0 + i]) * sl
+                     : 0.f;
+      o[h][i] = 0.f;
+    }
+    m[h] = -INFINITY;
+    z[h] = 0.f;
+  }
+  const T *k0 = kc + s.hk * pb.k_h, *v0 = vc + s.hk * pb.v_h;
+  for (int t0 = s.j0 + warp * KT; t0 < s.j1; t0 += kWarps * KT) {
+    const int2 at = place(pb, s, t0 + lane % KT, status);
+    float k[KT][CH], v[KT][CH];
+#pragma unroll
+    for (int y = 0; y < KT; ++y) {
+      const int page = __shfl_sync(0xffffffffu, at.x, y), row = __shfl_sync(0xffffffffu, at.y, y);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) k[y][i] = v[y][i] = 0.f;
+      if (page >= 0 && e0 < pb.d) {
+        const T* kr = k0 + page * pb.k_page + row * pb.k_n;
+        const T* vr = v0 + page * pb.v_page + row * pb.v_n;
+        if (vec) {
+          load_vector<T, CH>(k[y], kr + e0);
+          load_vector<T, CH>(v[y], vr + e0);
         } else {
-          atomicCAS(status, 0, kBadIndex);
+          load_channels<T, CH>(k[y], kr, e0, pb.d, false);
+          load_channels<T, CH>(v[y], vr, e0, pb.d, false);
         }
       }
-      sK[r * kPitch + e] = kv;
-      sV[r * kPitch + e] = vv;
     }
-    __syncthreads();
-    for (int h = warp; h < kHeads; h += kThreads / 32) {  // lane = key
-      float s = 0.f;
-#pragma unroll 4
-      for (int e = 0; e < DP; e += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(sQ + h * DP + e);
-        const float4 w = *reinterpret_cast<const float4*>(sK + lane * kPitch + e);
-        s = fmaf(a.x, w.x, s);
-        s = fmaf(a.y, w.y, s);
-        s = fmaf(a.z, w.z, s);
-        s = fmaf(a.w, w.w, s);
+    float w[kVals];  // product of key y and head h at y * GH + h
+#pragma unroll
+    for (int y = 0; y < KT; ++y)
+#pragma unroll
+      for (int h = 0; h < GH; ++h) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) a = fmaf(qr[h][i], k[y][i], a);
+        w[y * GH + h] = a;
       }
-      s = t0 + lane < j1 ? s * sl : -INFINITY;
-      const float m0 = sM[h], mn = fmaxf(m0, warp_max(s));
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float p = exp2f(s - base);
-      sP[h * kTile + lane] = p;
-      const float z = warp_sum(p), corr = exp2f(m0 - base);
-      __syncwarp();
-      if (lane == 0) {
-        sM[h] = mn;
-        sZ[h] = sZ[h] * corr + z;
-        sC[h] = corr;
+    // value x ends on the lanes whose top bits spell it, highest bit first
+    int bit = 16;
+#pragma unroll
+    for (int left = kVals; left > 1; left >>= 1, bit >>= 1) {
+      const bool up = lane & bit;
+#pragma unroll
+      for (int x = 0; x < left / 2; ++x) {
+        const float keep = up ? w[x + left / 2] : w[x], give = up ? w[x] : w[x + left / 2];
+        w[x] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
       }
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const int e = tid + i * kThreads;
-      if (e >= DP) break;
+    for (; bit > 0; bit >>= 1) w[0] += __shfl_xor_sync(0xffffffffu, w[0], bit);
+    constexpr int kStep = 32 / kVals;  // lanes of a value
+    const int mine = lane / kStep;
+    float sc = t0 + mine / GH < s.j1 ? w[0] : -INFINITY;
+    // maximum of each head over the keys: lanes GH * kStep apart
+    float mt = sc;
 #pragma unroll
-      for (int h = 0; h < kHeads; ++h) o[i][h] *= sC[h];
-      for (int r = 0; r < kTile; ++r) {
-        const float w = sV[r * kPitch + e];
+    for (int x = GH * kStep; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+    float base[GH];
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) o[i][h] = fmaf(sP[h * kTile + r], w, o[i][h]);
+    for (int h = 0; h < GH; ++h) {
+      const float mn = fmaxf(m[h], __shfl_sync(0xffffffffu, mt, h * kStep));
+      base[h] = mn == -INFINITY ? 0.f : mn;
+      if (mn > m[h]) {
+        const float f = exp2f(m[h] - base[h]);
+        z[h] *= f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[h][i] *= f;
+        m[h] = mn;
       }
+    }
+    float mb = base[0];
+#pragma unroll
+    for (int h = 1; h < GH; ++h)
+      if (mine % GH == h) mb = base[h];
+    const float p = exp2f(sc - mb);
+#pragma unroll
+    for (int y = 0; y < KT; ++y)
+#pragma unroll
+      for (int h = 0; h < GH; ++h) {
+        const float a = __shfl_sync(0xffffffffu, p, (y * GH + h) * kStep);
+        z[h] += a;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) o[h][i] = fmaf(a, v[y][i], o[h][i]);
+      }
+  }
+#pragma unroll
+  for (int h = 0; h < GH; ++h) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) so[warp][h][e0 + i] = o[h][i];
+    if (lane == 0) {
+      sm[warp][h] = m[h];
+      sz[warp][h] = z[h];
     }
   }
   __syncthreads();
-  const long at = ((long)c * pb.B + b) * pb.H + h0;
-  if (tid < nh) part_ml[at + tid] = make_float2(sM[tid], sZ[tid]);
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) {
-    const int e = tid + i * kThreads;
-    if (e < pb.d)
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h)
-        if (h < nh) part_o[(at + h) * pb.d + e] = o[i][h];
-  }
+  join_warps<T>(sm, sz, &so[0][0][0], GH * (DP + 4), DP + 4, pb, sp, s, part, out, lse);
 }
 
-// One warp per (b, h): the chunks' results weighted by exp(m - max) and summed.
+// One CTA per (b, h): the chunks' results weighted by exp2(m - max) and
+// summed in order, groups of threads taking every G-th chunk.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    decode_join_kernel(T* __restrict__ out, float* __restrict__ lse,
-                       const float2* __restrict__ part_ml, const float* __restrict__ part_o,
+    decode_join_kernel(T* __restrict__ out, float* __restrict__ lse, Parts part,
                        DecodeProblem pb, Split sp) {
-  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= pb.B * pb.H) return;
+  extern __shared__ float sw[];  // weight of each chunk
+  __shared__ float red[2][kWarps];
+  __shared__ float acc_s[kThreads][2];
+  tc::pdl_wait();
+  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = row / pb.H, h = row % pb.H;
   const int len = min(max(__ldg(pb.lens + b), 0), pb.max_pages * pb.page_size);
   const int n = (len + sp.chunk - 1) / sp.chunk;
   const long step = (long)pb.B * pb.H;
   float m = -INFINITY;
-  for (int c = lane; c < n; c += 32) m = fmaxf(m, part_ml[c * step + row].x);
+  for (int c = tid; c < n; c += kThreads) m = fmaxf(m, part.ml[c * step + row].x);
   m = warp_max(m);
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   const float base = m == -INFINITY ? 0.f : m;
   float z = 0.f;
-  for (int c = lane; c < n; c += 32) {
-    const float2 ml = part_ml[c * step + row];
-    z += ml.y * exp2f(ml.x - base);
+  for (int c = tid; c < n; c += kThreads) {
+    const float2 ml = part.ml[c * step + row];
+    const float f = exp2f(ml.x - base);
+    sw[c] = f;
+    z = fmaf(ml.y, f, z);
   }
   z = warp_sum(z);
-  for (int e = lane; e < pb.d; e += 32) {
-    float acc = 0.f;
-    for (int c = 0; c < n; ++c)
-      acc = fmaf(part_o[(c * step + row) * pb.d + e], exp2f(part_ml[c * step + row].x - base), acc);
-    out[b * pb.out_b + h * pb.out_h + e] = from_f32<T>(n > 0 ? acc / z : 0.f);
+  if (lane == 0) red[1][warp] = z;
+  __syncthreads();
+  z = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  // 32, 64 or 128 threads per chunk, up to two channels each
+  const int width = pb.d <= 32 ? 32 : pb.d <= 64 ? 64 : 128, groups = kThreads / width;
+  const int e = tid % width, first = tid / width;
+  const float* po = part.o + (long)row * pb.d;
+  float a0 = 0.f, a1 = 0.f;
+#pragma unroll 8
+  for (int c = first; c < n; c += groups) {
+    const float f = sw[c];
+    const float* p = po + c * step * pb.d;
+    if (e < pb.d) a0 = fmaf(p[e], f, a0);
+    if (e + width < pb.d) a1 = fmaf(p[e + width], f, a1);
   }
-  if (lane == 0) lse[row] = n > 0 ? (m + log2f(z)) * kLn2 : -INFINITY;
+  acc_s[tid][0] = a0;
+  acc_s[tid][1] = a1;
+  __syncthreads();
+  for (int x = tid; x < pb.d; x += kThreads) {
+    float a = 0.f;
+    for (int g = 0; g < groups; ++g) a += acc_s[g * width + x % width][x / width];
+    out[b * pb.out_b + h * pb.out_h + x] = from_f32<T>(n > 0 ? a / z : 0.f);
+  }
+  if (tid == 0) lse[row] = n > 0 ? (m + log2f(z)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int DP>
-cudaError_t forward_dp(const T* q, const T* k, const T* v, T* out, float* lse,
-                       const DecodeProblem& pb, float* ws, int* status, cudaStream_t stream,
-                       int* launches) {
-  const Split sp = make_split(pb);
-  const long rows = (long)sp.chunks * pb.B * pb.H;
-  float2* ml = reinterpret_cast<float2*>(ws);
-  float* po = ws + 2 * rows;
-  const size_t smem = (kHeads * DP + 2 * kTile * (DP + 4) + kHeads * kTile) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, DP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+bool rows_allow(const void* p, std::initializer_list<long> strides, long elements, size_t elt) {
+  if (reinterpret_cast<uintptr_t>(p) % (elements * elt)) return false;
+  for (long s : strides)
+    if (s % elements) return false;
+  return true;
+}
+
+template <int DP>
+cudaError_t launch_mma(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
+                       const DecodeProblem& pb, const Split& sp, Parts part, int* status,
+                       cudaStream_t stream, int* launches) {
+  const int smem = kWarps * MmaTile<DP>::kWarpBytes;
+  const cudaError_t e = cudaFuncSetAttribute(decode_mma_kernel<DP>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)((long)sp.chunks * sp.hg * pb.Hkv * pb.B);
-  e = timed_launch("decode_simt", stream, launches, [&] {
-    decode_kernel<T, DP><<<grid, kThreads, smem, stream>>>(q, k, v, ml, po, pb, sp, status);
+  const int hgs = (pb.H / pb.Hkv + kRows - 1) / kRows;
+  const unsigned grid = (unsigned)((long)sp.chunks * hgs * pb.Hkv * pb.B);
+  return timed_launch("decode_mma", stream, launches, [&] {
+    decode_mma_kernel<DP><<<grid, kThreads, smem, stream>>>(q, k, v, part, out, lse, pb, sp,
+                                                            status);
   });
-  if (e != cudaSuccess) return e;
-  const unsigned joins = (unsigned)((pb.B * pb.H + kThreads / 32 - 1) / (kThreads / 32));
-  return timed_launch("decode_join", stream, launches, [&] {
-    decode_join_kernel<T><<<joins, kThreads, 0, stream>>>(out, lse, ml, po, pb, sp);
+}
+
+template <typename T, int DP, int GH, int KT>
+cudaError_t launch_simt(const T* q, const T* k, const T* v, T* out, float* lse,
+                        const DecodeProblem& pb, const Split& sp, Parts part, int* status,
+                        cudaStream_t stream, int* launches) {
+  constexpr long CH = DP / 32, kVec = CH * sizeof(T) > 16 ? 16 / sizeof(T) : CH;
+  const bool vec = pb.d % CH == 0 && rows_allow(k, {pb.k_page, pb.k_h, pb.k_n}, kVec, sizeof(T)) &&
+                   rows_allow(v, {pb.v_page, pb.v_h, pb.v_n}, kVec, sizeof(T));
+  const int hgs = (pb.H / pb.Hkv + GH - 1) / GH;
+  const unsigned grid = (unsigned)((long)sp.chunks * hgs * pb.Hkv * pb.B);
+  return timed_launch("decode_simt", stream, launches, [&] {
+    decode_simt_kernel<T, DP, GH, KT><<<grid, kThreads, 0, stream>>>(q, k, v, part, out, lse, pb,
+                                                                    sp, vec, status);
   });
+}
+
+// One head, or up to four heads of a group at a time; eight keys, and four
+// where a lane holds eight channels.
+template <typename T>
+cudaError_t launch_simt_dp(const T* q, const T* k, const T* v, T* out, float* lse,
+                           const DecodeProblem& pb, const Split& sp, Parts part, int* status,
+                           cudaStream_t stream, int* launches) {
+  const bool one = pb.H == pb.Hkv;
+#define MONARCH_DECODE(DP, GH, KT) \
+  launch_simt<T, DP, GH, KT>(q, k, v, out, lse, pb, sp, part, status, stream, launches)
+  if (pb.d <= 64) return one ? MONARCH_DECODE(64, 1, 8) : MONARCH_DECODE(64, 4, 8);
+  if (pb.d <= 128) return one ? MONARCH_DECODE(128, 1, 8) : MONARCH_DECODE(128, 4, 8);
+  return one ? MONARCH_DECODE(256, 1, 4) : MONARCH_DECODE(256, 4, 4);
+#undef MONARCH_DECODE
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(const DecodeProblem& pb) {
   const Split sp = make_split(pb);
-  return (size_t)sp.chunks * pb.B * pb.H * (pb.d + 2) * sizeof(float);
+  return sp.chunks == 1 ? 0 : (size_t)sp.chunks * pb.B * pb.H * (pb.d + 2) * sizeof(float);
 }
 
 template <typename T>
 cudaError_t decode_forward(const T* q, const T* k, const T* v, T* out, float* lse,
                            const DecodeProblem& pb, float* ws, int* status, cudaStream_t stream,
                            int* launches) {
-  if (pb.d <= 64) return forward_dp<T, 64>(q, k, v, out, lse, pb, ws, status, stream, launches);
-  if (pb.d <= 128) return forward_dp<T, 128>(q, k, v, out, lse, pb, ws, status, stream, launches);
-  return forward_dp<T, 256>(q, k, v, out, lse, pb, ws, status, stream, launches);
+  const Split sp = make_split(pb);
+  Parts part = {reinterpret_cast<float2*>(ws), nullptr};
+  if (sp.chunks > 1) part.o = ws + 2 * (size_t)sp.chunks * pb.B * pb.H;
+  cudaError_t e;
+  bool mma = false;
+  if constexpr (sizeof(T) == 2) {
+    mma = pb.d % 8 == 0 && pb.d <= 128 && rows_allow(q, {pb.q_b, pb.q_h}, 8, 2) &&
+          rows_allow(k, {pb.k_page, pb.k_h, pb.k_n}, 8, 2) &&
+          rows_allow(v, {pb.v_page, pb.v_h, pb.v_n}, 8, 2);
+    if (mma)
+      e = pb.d <= 64
+              ? launch_mma<64>(q, k, v, out, lse, pb, sp, part, status, stream, launches)
+              : launch_mma<128>(q, k, v, out, lse, pb, sp, part, status, stream, launches);
+  }
+  if (!mma) e = launch_simt_dp<T>(q, k, v, out, lse, pb, sp, part, status, stream, launches);
+  if (e != cudaSuccess || sp.chunks == 1) return e;
+  return timed_launch("decode_join", stream, launches, [&] {
+    return launch_pdl(decode_join_kernel<T>, dim3(pb.B * pb.H), dim3(kThreads),
+                      sp.chunks * sizeof(float), stream, out, lse, part, pb, sp);
+  });
 }
 
 template cudaError_t decode_forward<float>(const float*, const float*, const float*, float*,
