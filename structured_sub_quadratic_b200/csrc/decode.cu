@@ -59,13 +59,14 @@ __device__ __forceinline__ Share share_of(const DecodeProblem& pb, const Split& 
                                           int* status) {
   const int group = pb.H / pb.Hkv, hgs = (group + heads - 1) / heads;
   Share s;
+  // heads first: where a token's heads lie side by side, they are read together
   int x = blockIdx.x;
-  s.c = x % sp.chunks;
-  x /= sp.chunks;
   const int hg = x % hgs;
   x /= hgs;
   s.hk = x % pb.Hkv;
-  s.b = x / pb.Hkv;
+  x /= pb.Hkv;
+  s.c = x % sp.chunks;
+  s.b = x / sp.chunks;
   s.h0 = s.hk * group + hg * heads;
   s.nh = min(heads, (s.hk + 1) * group - s.h0);
   const int n = __ldg(pb.lens + s.b), top = pb.max_pages * pb.page_size;
@@ -178,7 +179,9 @@ struct MmaTile {
   static_assert(kRows * kPitch * 4 <= kWarpBytes, "the result reuses the warp's slots");
 };
 
-template <int DP>
+// WIDE: more than 8 heads (else rows 8-15 of the products are padding, and
+// their softmax is left out).
+template <int DP, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
     decode_mma_kernel(const bf16* __restrict__ q, const bf16* __restrict__ kc,
                       const bf16* __restrict__ vc, Parts part, bf16* __restrict__ out,
@@ -212,24 +215,45 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int n = max(0, ((s.j1 - s.j0 + L::kKeys - 1) / L::kKeys - warp + kWarps - 1) / kWarps);
   auto tile_key = [&](int i) { return s.j0 + (warp + i * kWarps) * L::kKeys; };
-  auto lookup = [&](int i) {  // lane = key
-    return i < n ? place(pb, s, tile_key(i) + (lane & (L::kKeys - 1)), status)
+  // Tiles start at multiples of their size: where pages hold whole tiles, one
+  // entry of the table places a tile, and lanes step by a fixed stride.
+  const bool whole = pb.page_size % L::kKeys == 0;
+  auto lookup = [&](int i) {  // of the tile's first key, or of key `lane` of it
+    return i < n ? place(pb, s, tile_key(i) + (whole ? 0 : lane & (L::kKeys - 1)), status)
                  : make_int2(-1, 0);
   };
+  constexpr int kCopies = L::kKeys * L::kUnits / 32, kStep = 32 / L::kUnits;
+  const int lr = lane / L::kUnits, lu = lane % L::kUnits;  // row and unit of the first copy
+  const bf16* k0 = kc + s.hk * pb.k_h + lu * 8;
+  const bf16* v0 = vc + s.hk * pb.v_h + lu * 8;
+  const bool in_row = lu * 8 < pb.d;
   auto fetch = [&](int i, int2 at) {
     if (i < n) {
       const uint32_t dst = ring32 + (i % L::kStages) * 2 * L::kHalf;
-      const bf16 *k0 = kc + s.hk * pb.k_h, *v0 = vc + s.hk * pb.v_h;
+      const int left = s.j1 - tile_key(i);
+      if (whole && left >= L::kKeys && at.x >= 0) {
+        const bf16* ks = k0 + at.x * pb.k_page + (at.y + lr) * pb.k_n;
+        const bf16* vs = v0 + at.x * pb.v_page + (at.y + lr) * pb.v_n;
 #pragma unroll
-      for (int x = 0; x < L::kKeys * L::kUnits / 32; ++x) {
-        const int r = (x * 32 + lane) / L::kUnits, u = lane % L::kUnits;
-        const int page = __shfl_sync(0xffffffffu, at.x, r), row = __shfl_sync(0xffffffffu, at.y, r);
-        const bool there = page >= 0 && u * 8 < pb.d;
-        const bf16* ks = there ? k0 + page * pb.k_page + row * pb.k_n + u * 8 : kc;
-        const bf16* vs = there ? v0 + page * pb.v_page + row * pb.v_n + u * 8 : vc;
-        const uint32_t o = dst + r * DP * 2 + ((u ^ (r & 7)) << 4);
-        copy16(o, ks, there);
-        copy16(o + L::kHalf, vs, there);
+        for (int x = 0; x < kCopies; ++x) {
+          const int r = x * kStep + lr;
+          const uint32_t o = dst + r * DP * 2 + ((lu ^ (r & 7)) << 4);
+          copy16(o, in_row ? ks : kc, in_row);
+          copy16(o + L::kHalf, in_row ? vs : vc, in_row);
+          ks += kStep * pb.k_n;
+          vs += kStep * pb.v_n;
+        }
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < kCopies; ++x) {
+          const int r = x * kStep + lr;
+          const int page = whole ? (r < left ? at.x : -1) : __shfl_sync(0xffffffffu, at.x, r);
+          const int row = whole ? at.y + r : __shfl_sync(0xffffffffu, at.y, r);
+          const bool there = page >= 0 && in_row;
+          const uint32_t o = dst + r * DP * 2 + ((lu ^ (r & 7)) << 4);
+          copy16(o, there ? k0 + page * pb.k_page + row * pb.k_n : kc, there);
+          copy16(o + L::kHalf, there ? v0 + page * pb.v_page + row * pb.v_n : vc, there);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -239,7 +263,8 @@ __global__ void __launch_bounds__(kThreads)
   for (int x = 0; x < DP / 8; ++x)
 #pragma unroll
     for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f;  // heads g and g + 8
+  // heads g and g + 8: maximum of the raw products, sum
+  float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f;
   const float sl = pb.scale * kLog2e;
 #pragma unroll
   for (int i = 0; i < L::kStages - 1; ++i) fetch(i, lookup(i));
@@ -265,25 +290,30 @@ __global__ void __launch_bounds__(kThreads)
         mma16816(c[x], qa[kk + 1], kb[2], kb[3]);
       }
     }
+    if (left < L::kKeys) {
+#pragma unroll
+      for (int x = 0; x < L::kKeys / 8; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (x * 8 + t4 * 2 + (y & 1) >= left) c[x][y] = -INFINITY;
+    }
     float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < L::kKeys / 8; ++x)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const bool see = x * 8 + t4 * 2 + y < left;
-        c[x][y] = see ? c[x][y] * sl : -INFINITY;
-        c[x][2 + y] = see ? c[x][2 + y] * sl : -INFINITY;
-        a0 = fmaxf(a0, c[x][y]);
-        a1 = fmaxf(a1, c[x][2 + y]);
-      }
+    for (int x = 0; x < L::kKeys / 8; ++x) {
+      a0 = tc::max3(a0, c[x][0], c[x][1]);
+      if (WIDE) a1 = tc::max3(a1, c[x][2], c[x][3]);
+    }
 #pragma unroll
     for (int x = 1; x < 4; x <<= 1) {
       a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, x));
-      a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, x));
+      if (WIDE) a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, x));
     }
-    if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
+    // The running maximum moves when it grows by 2^8 or more: weights then
+    // reach 256, exact in bf16's and fp32's exponents.
+    if (__any_sync(0xffffffffu, (a0 - m0) * sl > 8.f || (WIDE && (a1 - m1) * sl > 8.f))) {
       const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-      const float f0 = m0 == n0 ? 1.f : exp2f(m0 - n0), f1 = m1 == n1 ? 1.f : exp2f(m1 - n1);
+      const float f0 = m0 == n0 ? 1.f : tc::ex2((m0 - n0) * sl);
+      const float f1 = m1 == n1 ? 1.f : tc::ex2((m1 - n1) * sl);
       m0 = n0;
       m1 = n1;
       z0 *= f0;
@@ -292,23 +322,28 @@ __global__ void __launch_bounds__(kThreads)
       for (int x = 0; x < DP / 8; ++x) {
         o[x][0] *= f0;
         o[x][1] *= f0;
-        o[x][2] *= f1;
-        o[x][3] *= f1;
+        if (WIDE) {
+          o[x][2] *= f1;
+          o[x][3] *= f1;
+        }
       }
     }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+    const float b0 = m0 == -INFINITY ? 0.f : -m0 * sl, b1 = m1 == -INFINITY ? 0.f : -m1 * sl;
 #pragma unroll
     for (int kk = 0; kk < L::kKeys / 16; ++kk) {
       uint32_t pa[4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float* cc = c[kk * 2 + x];
-        const float p0 = tc::ex2(cc[0] - b0), p1 = tc::ex2(cc[1] - b0);
-        const float p2 = tc::ex2(cc[2] - b1), p3 = tc::ex2(cc[3] - b1);
+        const float p0 = tc::ex2(fmaf(cc[0], sl, b0)), p1 = tc::ex2(fmaf(cc[1], sl, b0));
         z0 += p0 + p1;
-        z1 += p2 + p3;
         pa[2 * x] = tc::pack_bf16x2(p0, p1);
-        pa[2 * x + 1] = tc::pack_bf16x2(p2, p3);
+        pa[2 * x + 1] = 0u;
+        if (WIDE) {
+          const float p2 = tc::ex2(fmaf(cc[2], sl, b1)), p3 = tc::ex2(fmaf(cc[3], sl, b1));
+          z1 += p2 + p3;
+          pa[2 * x + 1] = tc::pack_bf16x2(p2, p3);
+        }
       }
       const int r = kk * 16 + (lane & 15);
 #pragma unroll
@@ -328,8 +363,8 @@ __global__ void __launch_bounds__(kThreads)
     z1 += __shfl_xor_sync(0xffffffffu, z1, x);
   }
   if (t4 == 0) {
-    sm[warp][g] = m0;
-    sm[warp][g + 8] = m1;
+    sm[warp][g] = m0 * sl;
+    sm[warp][g + 8] = m1 * sl;
     sz[warp][g] = z0;
     sz[warp][g + 8] = z1;
   }
@@ -514,15 +549,16 @@ __global__ void __launch_bounds__(kThreads)
   join_warps<T>(sm, sz, &so[0][0][0], GH * (DP + 4), DP + 4, pb, sp, s, part, out, lse);
 }
 
-// One CTA per (b, h): the chunks' results weighted by exp2(m - max) and
-// summed in order, groups of threads taking every G-th chunk.
+// One CTA of eight warps per (b, h): the chunks' results weighted by
+// exp2(m - max); a warp sums every eighth chunk, then the warps are summed.
+constexpr int kJoinWarps = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     decode_join_kernel(T* __restrict__ out, float* __restrict__ lse, Parts part,
                        DecodeProblem pb, Split sp) {
-  extern __shared__ float sw[];  // weight of each chunk
-  __shared__ float red[2][kWarps];
-  __shared__ float acc_s[kThreads][2];
+  __shared__ float sm[kJoinWarps], sz[kJoinWarps];
+  __shared__ float sa[kJoinWarps][256];
   tc::pdl_wait();
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = row / pb.H, h = row % pb.H;
@@ -530,44 +566,39 @@ __global__ void __launch_bounds__(kThreads)
   const int n = (len + sp.chunk - 1) / sp.chunk;
   const long step = (long)pb.B * pb.H;
   float m = -INFINITY;
-  for (int c = tid; c < n; c += kThreads) m = fmaxf(m, part.ml[c * step + row].x);
+  for (int c = tid; c < n; c += 32 * kJoinWarps) m = fmaxf(m, part.ml[c * step + row].x);
   m = warp_max(m);
-  if (lane == 0) red[0][warp] = m;
+  if (lane == 0) sm[warp] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  m = warp_max(sm[lane % kJoinWarps]);
   const float base = m == -INFINITY ? 0.f : m;
-  float z = 0.f;
-  for (int c = tid; c < n; c += kThreads) {
+  float acc[8], z = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int c = warp; c < n; c += kJoinWarps) {
     const float2 ml = part.ml[c * step + row];
+    const float* p = part.o + (c * step + row) * pb.d;
     const float f = exp2f(ml.x - base);
-    sw[c] = f;
     z = fmaf(ml.y, f, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 32 + lane < pb.d) acc[i] = fmaf(p[i * 32 + lane], f, acc[i]);
   }
-  z = warp_sum(z);
-  if (lane == 0) red[1][warp] = z;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sa[warp][i * 32 + lane] = acc[i];
+  if (lane == 0) sz[warp] = z;
   __syncthreads();
-  z = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  // 32, 64 or 128 threads per chunk, up to two channels each
-  const int width = pb.d <= 32 ? 32 : pb.d <= 64 ? 64 : 128, groups = kThreads / width;
-  const int e = tid % width, first = tid / width;
-  const float* po = part.o + (long)row * pb.d;
-  float a0 = 0.f, a1 = 0.f;
-#pragma unroll 8
-  for (int c = first; c < n; c += groups) {
-    const float f = sw[c];
-    const float* p = po + c * step * pb.d;
-    if (e < pb.d) a0 = fmaf(p[e], f, a0);
-    if (e + width < pb.d) a1 = fmaf(p[e + width], f, a1);
-  }
-  acc_s[tid][0] = a0;
-  acc_s[tid][1] = a1;
-  __syncthreads();
-  for (int x = tid; x < pb.d; x += kThreads) {
+  float zz = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) zz += sz[w];
+  if (tid < pb.d) {
     float a = 0.f;
-    for (int g = 0; g < groups; ++g) a += acc_s[g * width + x % width][x / width];
-    out[b * pb.out_b + h * pb.out_h + x] = from_f32<T>(n > 0 ? a / z : 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) a += sa[w][tid];
+    out[b * pb.out_b + h * pb.out_h + tid] = from_f32<T>(n > 0 ? a / zz : 0.f);
   }
-  if (tid == 0) lse[row] = n > 0 ? (m + log2f(z)) * kLn2 : -INFINITY;
+  if (tid == 0) lse[row] = n > 0 ? (m + log2f(zz)) * kLn2 : -INFINITY;
 }
 
 bool rows_allow(const void* p, std::initializer_list<long> strides, long elements, size_t elt) {
@@ -577,19 +608,19 @@ bool rows_allow(const void* p, std::initializer_list<long> strides, long element
   return true;
 }
 
-template <int DP>
+template <int DP, bool WIDE>
 cudaError_t launch_mma(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
                        const DecodeProblem& pb, const Split& sp, Parts part, int* status,
                        cudaStream_t stream, int* launches) {
   const int smem = kWarps * MmaTile<DP>::kWarpBytes;
-  const cudaError_t e = cudaFuncSetAttribute(decode_mma_kernel<DP>,
+  const cudaError_t e = cudaFuncSetAttribute(decode_mma_kernel<DP, WIDE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int hgs = (pb.H / pb.Hkv + kRows - 1) / kRows;
   const unsigned grid = (unsigned)((long)sp.chunks * hgs * pb.Hkv * pb.B);
   return timed_launch("decode_mma", stream, launches, [&] {
-    decode_mma_kernel<DP><<<grid, kThreads, smem, stream>>>(q, k, v, part, out, lse, pb, sp,
-                                                            status);
+    decode_mma_kernel<DP, WIDE>
+        <<<grid, kThreads, smem, stream>>>(q, k, v, part, out, lse, pb, sp, status);
   });
 }
 
@@ -643,16 +674,18 @@ cudaError_t decode_forward(const T* q, const T* k, const T* v, T* out, float* ls
     mma = pb.d % 8 == 0 && pb.d <= 128 && rows_allow(q, {pb.q_b, pb.q_h}, 8, 2) &&
           rows_allow(k, {pb.k_page, pb.k_h, pb.k_n}, 8, 2) &&
           rows_allow(v, {pb.v_page, pb.v_h, pb.v_n}, 8, 2);
-    if (mma)
-      e = pb.d <= 64
-              ? launch_mma<64>(q, k, v, out, lse, pb, sp, part, status, stream, launches)
-              : launch_mma<128>(q, k, v, out, lse, pb, sp, part, status, stream, launches);
+    if (mma) {
+      const bool wide = pb.H / pb.Hkv > 8;
+      const auto launch = pb.d <= 64 ? (wide ? launch_mma<64, true> : launch_mma<64, false>)
+                                     : (wide ? launch_mma<128, true> : launch_mma<128, false>);
+      e = launch(q, k, v, out, lse, pb, sp, part, status, stream, launches);
+    }
   }
   if (!mma) e = launch_simt_dp<T>(q, k, v, out, lse, pb, sp, part, status, stream, launches);
   if (e != cudaSuccess || sp.chunks == 1) return e;
   return timed_launch("decode_join", stream, launches, [&] {
-    return launch_pdl(decode_join_kernel<T>, dim3(pb.B * pb.H), dim3(kThreads),
-                      sp.chunks * sizeof(float), stream, out, lse, part, pb, sp);
+    return launch_pdl(decode_join_kernel<T>, dim3(pb.B * pb.H), dim3(32 * kJoinWarps), 0,
+                      stream, out, lse, part, pb, sp);
   });
 }
 
