@@ -265,47 +265,61 @@ def monarch_attn_fwd_host(q, k, v, out, b1, b2, T, c1=1, c2=1, stream=None):
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
+def _elsewhere(t, stream):
+    """Whether t's device or `stream` is not the current one (see _at)."""
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {t.device}")
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """`device` current and, if given, `stream` too: what is allocated inside
-    belongs to the stream that uses it."""
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+def _at(t, stream):
+    """t's device current and, if given, `stream` too: what a call allocates
+    inside belongs to the stream that uses it."""
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
         yield
 
 
-def _scope(t, stream):
-    """Context of a call on t's device (nothing to do where it is current)."""
-    if stream is not None and stream.device != t.device:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {t.device}")
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _on(t.device, stream)
+def _current(device_index):
+    """The current stream's handle (torch.cuda.current_stream without its object)."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
 
 
 def _dense_dtype(name, like, *tensors):
     """The dtype code of `like` after checking that each tensor shares its
     dtype and CUDA device and has contiguous channels."""
-    dtype = _DTYPES.get(like.dtype)
+    dtype, kind, device = _DTYPES.get(like.dtype), like.dtype, like.get_device()
     if dtype is None:
         raise ValueError(f"unsupported dtype {like.dtype}")
     for t in (like, *tensors):
-        if t.dtype != like.dtype or not t.is_cuda or t.device != like.device:
+        if t.dtype != kind or t.get_device() != device or device < 0:
             raise ValueError(f"{name} must be CUDA tensors of one dtype on one device")
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{name} must have contiguous channels (last stride 1)")
     return dtype
 
 
-def _int_tensor(name, t, device, shape):
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape \
+def _int_tensor(name, t, like, shape):
+    if t.dtype != torch.int32 or t.get_device() != like.get_device() or t.shape != shape \
             or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {shape} on {device}")
+        raise ValueError(f"{name} must be a contiguous int32 tensor {shape} on {like.device}")
     return t.data_ptr()
+
+
+_STRIDES = {n: _L * (3 * n) for n in (4, 8)}
 
 
 def _strides(*tensors):
     """Batch, head and token strides of (B, H, N, d) tensors for the C ABI."""
-    return (_L * (3 * len(tensors)))(*(s for t in tensors for s in t.stride()[:3]))
+    flat = []
+    for t in tensors:
+        flat += t.stride()[:3]
+    return _STRIDES[len(tensors)](*flat)
+
+
+def _like(t):
+    """Uninitialised, t's shape, and t's strides unless its elements repeat."""
+    return t.new_empty(t.shape) if 0 in t.stride() else torch.empty_like(t)
 
 
 def _dense_dims(q, k, v, scale):
@@ -337,15 +351,17 @@ def monarch_attn_dense_fwd(q, k, v, causal=False, k_lens=None, scale=None, out=N
     dtype = _dense_dtype("q, k, v and out", q, k, v, *(() if out is None else (out,)))
     if out is not None and out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    lens = None if k_lens is None else _int_tensor("k_lens", k_lens, q.device, (B,))
-    with _scope(q, stream):
-        if out is None:
-            out = torch.empty_like(q) if _own_memory(q) else q.new_empty(q.shape)
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-        _check(lib.monarch_attn_dense_fwd(
-            dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
-            Hkv, Nq, Nk, d, _strides(q, k, v, out), bool(causal), lens, scale,
-            _stream_ptr(stream)))
+    lens = None if k_lens is None else _int_tensor("k_lens", k_lens, q, (B,))
+    if _elsewhere(q, stream):
+        with _at(q, stream):
+            return monarch_attn_dense_fwd(q, k, v, causal, k_lens, scale, out)
+    if out is None:
+        out = _like(q)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    _check(lib.monarch_attn_dense_fwd(
+        dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
+        Hkv, Nq, Nk, d, _strides(q, k, v, out), bool(causal), lens, scale,
+        _current(q.get_device())))
     return out, lse
 
 
@@ -363,23 +379,25 @@ def monarch_attn_dense_bwd(q, k, v, out, lse, dout, causal=False, k_lens=None, s
     if lse.dtype != torch.float32 or lse.shape != (B, H, Nq) or lse.device != q.device \
             or not lse.is_contiguous():
         raise ValueError("lse must be the contiguous fp32 (B, H, Nq) tensor of the forward pass")
-    lens = None if k_lens is None else _int_tensor("k_lens", k_lens, q.device, (B,))
-    with _scope(q, stream):
-        dq, dk, dv = (torch.empty_like(t) if _own_memory(t) else
-                      torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        need = lib.monarch_attn_dense_bwd_workspace_bytes(B, H, Nq)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _check(lib.monarch_attn_dense_bwd(
-            dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Nq, Nk, d,
-            _strides(q, k, v, out, dout, dq, dk, dv), bool(causal), lens, scale, ws.data_ptr(),
-            need, _stream_ptr(stream)))
+    lens = None if k_lens is None else _int_tensor("k_lens", k_lens, q, (B,))
+    if _elsewhere(q, stream):
+        with _at(q, stream):
+            return monarch_attn_dense_bwd(q, k, v, out, lse, dout, causal, k_lens, scale)
+    dq, dk, dv = _like(q), _like(k), _like(v)
+    need = lib.monarch_attn_dense_bwd_workspace_bytes(B, H, Nq)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib.monarch_attn_dense_bwd(
+        dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Nq, Nk, d,
+        _strides(q, k, v, out, dout, dq, dk, dv), bool(causal), lens, scale, ws.data_ptr(), need,
+        _current(q.get_device())))
     return dq, dk, dv
 
 
-def _own_memory(t):
-    """No element of t repeats another (no expanded dimension)."""
-    return all(s > 0 or n <= 1 for s, n in zip(t.stride(), t.shape))
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(device_index, *sizes):
+    """Bytes that a decode call of these sizes needs (a function of the sizes and the device)."""
+    return load_library().monarch_attn_dense_decode_workspace_bytes(*sizes)
 
 
 def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None, out=None,
@@ -409,23 +427,23 @@ def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None,
     if page_table.dim() != 2:
         raise ValueError("page_table must be (B, max_pages)")
     max_pages = page_table.shape[1]
-    table = _int_tensor("page_table", page_table, q.device, (B, max_pages))
-    lens = _int_tensor("lens", lens, q.device, (B,))
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _scope(q, stream):
-        if out is None:
-            out = torch.empty_like(q) if _own_memory(q) else q.new_empty(q.shape)
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        need = lib.monarch_attn_dense_decode_workspace_bytes(dtype, B, H, Hkv, d, page_size,
-                                                             max_pages)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        sq, so, sk, sv = q.stride(), out.stride(), k_cache.stride(), v_cache.stride()
-        strides = (_L * 12)(sq[0], sq[1], 0, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], so[0],
-                            so[1], 0)
-        _check(lib.monarch_attn_dense_decode(
-            dtype, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, lens,
-            out.data_ptr(), lse.data_ptr(), B, H, Hkv, d, pages, page_size, max_pages, strides,
-            scale, ws.data_ptr(), need, _stream_ptr(stream)))
+    table = _int_tensor("page_table", page_table, q, (B, max_pages))
+    len_ptr = _int_tensor("lens", lens, q, (B,))
+    if _elsewhere(q, stream):
+        with _at(q, stream):
+            return monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale, out)
+    if out is None:
+        out = _like(q)
+    lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    need = _decode_workspace(q.get_device(), dtype, B, H, Hkv, d, page_size, max_pages)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    strides = _STRIDES[4](*q.stride()[:2], 0, *k_cache.stride()[:3], *v_cache.stride()[:3],
+                          *out.stride()[:2], 0)
+    _check(lib.monarch_attn_dense_decode(
+        dtype, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, len_ptr,
+        out.data_ptr(), lse.data_ptr(), B, H, Hkv, d, pages, page_size, max_pages, strides,
+        1.0 / math.sqrt(d) if scale is None else scale, ws.data_ptr(), need,
+        _current(q.get_device())))
     return out, lse
 
 
@@ -514,22 +532,26 @@ def monarch_attn_rotary(q, k=None, positions=None, *, axis_dims=None, grid=None,
             shape = (N,)
         elif positions.dim() == 3:
             shape, step = (B, *shape), len(axis_dims) * N
-        where = _int_tensor("positions", positions, q.device, shape)
+        where = _int_tensor("positions", positions, q, shape)
+    if _elsewhere(q, stream):
+        with _at(q, stream):
+            return monarch_attn_rotary(q, k, positions, axis_dims=axis_dims, grid=grid,
+                                       interleaved=interleaved, base=base, scaling=scaling,
+                                       inverse=inverse, q_out=q_out, k_out=k_out)
     dims, freqs, magnitude = _rotary_args(axis_dims, base, scaling)
-    with _scope(q, stream):
-        if q_out is None:
-            q_out = torch.empty_like(q) if _own_memory(q) else q.new_empty(q.shape)
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k) if _own_memory(k) else k.new_empty(k.shape)
-        if k is None:
-            heads, kp, kop, strides = 0, None, None, _strides(q, q_out, q, q_out)
-        else:
-            heads, kp, kop = k.shape[1], k.data_ptr(), k_out.data_ptr()
-            strides = _strides(q, q_out, k, k_out)
-        _check(lib.monarch_attn_rotary(
-            dtype, q.data_ptr(), kp, q_out.data_ptr(), kop, B, H, heads, N, d, strides,
-            len(axis_dims), dims, sizes, where, step, freqs, magnitude, bool(interleaved),
-            bool(inverse), _stream_ptr(stream)))
+    if q_out is None:
+        q_out = _like(q)
+    if k is None:
+        heads, kp, kop, strides = 0, None, None, _strides(q, q_out, q, q_out)
+    else:
+        if k_out is None:
+            k_out = _like(k)
+        heads, kp, kop = k.shape[1], k.data_ptr(), k_out.data_ptr()
+        strides = _strides(q, q_out, k, k_out)
+    _check(lib.monarch_attn_rotary(
+        dtype, q.data_ptr(), kp, q_out.data_ptr(), kop, B, H, heads, N, d, strides,
+        len(axis_dims), dims, sizes, where, step, freqs, magnitude, bool(interleaved),
+        bool(inverse), _current(q.get_device())))
     return q_out, k_out
 
 

@@ -613,8 +613,7 @@ cudaError_t launch_mma(const bf16* q, const bf16* k, const bf16* v, bf16* out, f
                        const DecodeProblem& pb, const Split& sp, Parts part, int* status,
                        cudaStream_t stream, int* launches) {
   const int smem = kWarps * MmaTile<DP>::kWarpBytes;
-  const cudaError_t e = cudaFuncSetAttribute(decode_mma_kernel<DP, WIDE>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<decode_mma_kernel<DP, WIDE>>(smem);
   if (e != cudaSuccess) return e;
   const int hgs = (pb.H / pb.Hkv + kRows - 1) / kRows;
   const unsigned grid = (unsigned)((long)sp.chunks * hgs * pb.Hkv * pb.B);

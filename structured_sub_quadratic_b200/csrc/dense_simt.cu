@@ -13,6 +13,7 @@
 
 #include <math.h>
 
+#include "launch.cuh"
 #include "timing.cuh"
 
 namespace monarch {
@@ -417,16 +418,11 @@ bool rows_allow_four(const void* p, const HeadStrides& s, size_t elt) {
          s.n % 4 == 0;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <typename T, int DP>
 cudaError_t forward_dp(const T* q, const T* k, const T* v, T* out, float* lse,
                        const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
   const size_t smem = (3 * 64 * (DP + 4) + 64 * 68) * sizeof(float);
-  cudaError_t e = allow_smem(dense_fwd_kernel<T, DP>, smem);
+  cudaError_t e = allow_smem<dense_fwd_kernel<T, DP>>((int)smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((pb.Nq + 63) / 64) * pb.H * pb.B;
   return timed_launch("dense_fwd_simt", stream, launches, [&] {
@@ -442,7 +438,7 @@ cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, co
   const size_t qs = (4 * BT * (DP + 4) + BT * (BT + 4)) * sizeof(float);
   cudaError_t e = cudaSuccess;
   if (pb.Nk > 0) {
-    if ((e = allow_smem(dense_dkv_kernel<T, DP, BT>, kv)) != cudaSuccess) return e;
+    if ((e = allow_smem<dense_dkv_kernel<T, DP, BT>>((int)kv)) != cudaSuccess) return e;
     e = timed_launch("dense_dkv_simt", stream, launches, [&] {
       dense_dkv_kernel<T, DP, BT>
           <<<(unsigned)((pb.Nk + BT - 1) / BT) * pb.Hkv * pb.B, kThreads, kv, stream>>>(
@@ -451,7 +447,7 @@ cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, co
     if (e != cudaSuccess) return e;
   }
   if (pb.Nq > 0) {
-    if ((e = allow_smem(dense_dq_kernel<T, DP, BT>, qs)) != cudaSuccess) return e;
+    if ((e = allow_smem<dense_dq_kernel<T, DP, BT>>((int)qs)) != cudaSuccess) return e;
     e = timed_launch("dense_dq_simt", stream, launches, [&] {
       dense_dq_kernel<T, DP, BT>
           <<<(unsigned)((pb.Nq + BT - 1) / BT) * pb.H * pb.B, kThreads, qs, stream>>>(

@@ -982,8 +982,7 @@ template <int D>
 cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mo,
                       const FwdArgs& a, cudaStream_t stream, int* launches) {
   using L = FwdLayout<D>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      dense_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  const cudaError_t e = allow_smem<dense_fwd_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)a.tiles * a.pb.H * a.pb.B;
   return timed_launch("dense_fwd_tc", stream, launches, [&] {
@@ -996,8 +995,7 @@ cudaError_t backward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, 
                        const TileMap& mdq, const TileMap& mdk, const TileMap& mdv, BwdArgs a,
                        cudaStream_t stream, int* launches) {
   using L = BwdLayout<D>;
-  cudaError_t e = cudaFuncSetAttribute(dense_dkv_tc_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  cudaError_t e = allow_smem<dense_dkv_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
   a.tiles = (a.pb.Nk + kTile - 1) / kTile;
   e = timed_launch("dense_dkv_tc", stream, launches, [&] {
@@ -1005,10 +1003,7 @@ cudaError_t backward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, 
                              stream>>>(mq, mk, mv, mg, mdk, mdv, a);
   });
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(dense_dq_tc_kernel<D>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes)) !=
-      cudaSuccess)
-    return e;
+  if ((e = allow_smem<dense_dq_tc_kernel<D>>(L::kBytes)) != cudaSuccess) return e;
   a.tiles = (a.pb.Nq + kTile - 1) / kTile;
   return timed_launch("dense_dq_tc", stream, launches, [&] {
     dense_dq_tc_kernel<D><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
