@@ -101,7 +101,8 @@ struct RotaryProblem {
   long pos_b;             // elements between batches (0: shared)
   int interleaved, inverse;
   float magnitude;
-  double turns[kRotaryPairs];  // frequency / (2 pi) of each pair, axis after axis
+  // turns per position of each pair, axis after axis, modulo 1, in units of 2^-64
+  unsigned long long turns[kRotaryPairs];
 };
 
 template <typename T>

@@ -404,7 +404,10 @@ int monarch_attn_rotary(int dtype, const void* q, const void* k, void* q_out, vo
   if (pb.rot > d || (grid && tokens != N)) return MONARCH_ERR_INVALID_ARG;
   for (int r = 0; r < pb.rot / 2; ++r) {
     if (!isfinite(freqs[r])) return MONARCH_ERR_INVALID_ARG;
-    pb.turns[r] = freqs[r] / (2 * 3.14159265358979323846);
+    // whole turns per position leave the angle as it is
+    const long double t = freqs[r] / (2 * 3.14159265358979323846264338328L);
+    const long double part = t - floorl(t);
+    pb.turns[r] = part < 1 ? (unsigned long long)ldexpl(part, 64) : 0;
   }
   pb.positions = positions;
   pb.pos_b = positions_batch_stride;

@@ -6,9 +6,10 @@
 // per position axis; a pair is two neighbours of a section (interleaved) or
 // the same place of its two halves.  The other channels are copied.
 //
-// Angles are far too large for 32 bits (a position of 10^6 leaves 2^-4 rad):
-// position * (frequency / 2 pi) is formed and reduced to a fraction of a turn
-// in 64 bits, then sincospi runs in 32 on a value in [-1, 1] (error 1e-7).
+// Angles are far too large for 32 bits (a position of 10^6 leaves 2^-4 rad).
+// A frequency is held as a fraction of a turn in units of 2^-64, so that
+// position * frequency modulo 2^64 is the angle reduced to one turn, off by
+// 2^-34 turns for any 32-bit position; its top 32 bits go to sincospi.
 //
 // A thread keeps one place of one token (a unit: a pair, or 16-byte chunks of
 // pairs) and its cosines and sines in registers, and walks the heads of q and
@@ -35,22 +36,54 @@ constexpr int kBatch = 4;  // heads whose loads are in flight together
 //   kHalves       a chunk of first members and the chunk of their partners
 enum class Unit { kPairs, kInterleaved, kHalves };
 
-// Cosine and sine of pair r of an axis at `position`.
+// Cosine and sine of pair r at `position`.
 __device__ __forceinline__ float2 turn(const RotaryProblem& pb, int r, int position) {
-  double t = position * pb.turns[r];
-  t -= rint(t);
+  const unsigned long long t = (unsigned long long)(long long)position * pb.turns[r];
   float s, c;
-  sincospif(2.f * (float)t, &s, &c);
+  sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);  // half turns in [-1, 1]
   if (pb.inverse) s = -s;
   return make_float2(c * pb.magnitude, s * pb.magnitude);
 }
 
-__device__ __forceinline__ int token_position(const RotaryProblem& pb, int b, int n, int axis) {
-  if (pb.positions) return __ldg(pb.positions + b * pb.pos_b + (long)axis * pb.N + n);
-  int inner = 1;
-  for (int a = pb.axes - 1; a > axis; --a) inner *= pb.grid[a];
-  return n / inner % pb.grid[axis];
-}
+// The positions of one token.
+struct Place {
+  int p[kRotaryAxes];
+
+  __device__ __forceinline__ Place(const RotaryProblem& pb, int b, int n) {
+#pragma unroll
+    for (int a = kRotaryAxes - 1; a >= 0; --a) {
+      p[a] = 0;
+      if (a >= pb.axes) continue;
+      if (pb.positions) {
+        p[a] = __ldg(pb.positions + b * pb.pos_b + (long)a * pb.N + n);
+      } else {
+        const int outer = n / pb.grid[a];
+        p[a] = n - outer * pb.grid[a];
+        n = outer;
+      }
+    }
+  }
+};
+
+// Where channel c < rot lies: its section's start and half, and its position.
+struct Section {
+  int start, half, position;
+
+  __device__ __forceinline__ Section(const RotaryProblem& pb, const Place& at, int c) {
+    start = 0;
+    half = pb.dims[0] / 2;
+    position = at.p[0];
+    int end = pb.dims[0];
+#pragma unroll
+    for (int a = 1; a < kRotaryAxes; ++a)
+      if (a < pb.axes && c >= end) {
+        start = end;
+        half = pb.dims[a] / 2;
+        position = at.p[a];
+        end += pb.dims[a];
+      }
+  }
+};
 
 template <typename T, int E>
 struct alignas(E == 1 ? sizeof(T) : 16) Chunk {  // 16 bytes, or one element
@@ -88,6 +121,7 @@ __global__ void __launch_bounds__(kThreads)
   const long token = (long)blockIdx.x * sh.tokens + threadIdx.x / sh.units;
   if ((int)threadIdx.x >= sh.units * sh.tokens || token >= (long)pb.B * pb.N) return;
   const int n = (int)(token % pb.N), b = (int)(token / pb.N);
+  const Place place(pb, b, n);
 
   // The unit's first channels (`first`, and `second` of its partners, -1 for
   // none) and turns.  Pairs are counted axis after axis, then what is copied.
@@ -99,26 +133,20 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kTurns; ++i) {
       const int c = first + 2 * i;  // a section starts at an even channel
       if (c < pb.rot) {
-        int axis = 0, start = 0;
-        while (c >= start + pb.dims[axis]) start += pb.dims[axis++];
-        w[i] = turn(pb, c / 2, token_position(pb, b, n, axis));
+        w[i] = turn(pb, c / 2, Section(pb, place, c).position);
         rotated = i + 1;
       }
     }
   } else {
-    int axis = 0, start = 0, r = u * E;
-    while (axis < pb.axes && r >= pb.dims[axis] / 2) {
-      r -= pb.dims[axis] / 2;
-      start += pb.dims[axis++];
-    }
-    if (axis < pb.axes) {
-      first = pb.interleaved ? start + 2 * r : start + r;
-      second = pb.interleaved ? first + 1 : first + pb.dims[axis] / 2;
-      const int position = token_position(pb, b, n, axis);
+    const int r = u * E;
+    if (2 * r < pb.rot) {
+      const Section s(pb, place, 2 * r);  // pair r has channel 2 r of its section, interleaved
+      first = pb.interleaved ? 2 * r : s.start / 2 + r;
+      second = pb.interleaved ? first + 1 : first + s.half;
 #pragma unroll
-      for (int i = 0; i < kTurns; ++i) w[i] = turn(pb, start / 2 + r + i, position);
+      for (int i = 0; i < kTurns; ++i) w[i] = turn(pb, r + i, s.position);
     } else {
-      first = start + r;
+      first = pb.rot / 2 + r;
     }
   }
 
@@ -169,99 +197,80 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Halves whose size is no whole chunk (three axes of a 128-channel head, say):
-// a warp takes the rows of a few tokens that fill 32 chunks, reads and writes
-// them as chunks, and turns the pairs in shared memory in between.
+// a warp takes the rows of a few tokens that fill up to 32 chunks, one a lane.
+// Each lane turns the channels of its own chunk, x cos t -+ partner sin t, and
+// reads the partners, wherever they lie, from the warp's chunks in shared
+// memory.  Word w of lane i's chunk sits at 32 w + i, so that lanes reading
+// the same place of their chunks touch different banks.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     rotary_staged_kernel(const T* q, const T* k, T* qo, T* ko,
                          const __grid_constant__ RotaryProblem pb, Shape sh) {
-  constexpr int E = 16 / (int)sizeof(T);
-  constexpr int kChunks = 64, kPairs = 4;  // of a warp; of a lane (32 chunks hold 128 pairs)
-  __shared__ Chunk<T, E> buf[kThreads / 32][kBatch][kChunks];
+  constexpr int E = 16 / (int)sizeof(T), kPerWord = 4 / (int)sizeof(T);
+  __shared__ uint32_t buf[kThreads / 32][kBatch][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row_chunks = pb.d / E, row_pairs = pb.rot / 2;
   const long t0 = ((long)blockIdx.x * (kThreads / 32) + warp) * sh.tokens;
   const int rows = (int)min((long)sh.tokens, (long)pb.B * pb.N - t0);
-  if (rows <= 0) return;
-  auto place = [&](int row, int* b) {  // token of a row, and its batch
-    *b = (int)((t0 + row) / pb.N);
-    return (int)((t0 + row) % pb.N);
+  if (rows <= 0) return;  // (whole warps)
+  const int row = lane / sh.units, first = lane % sh.units * E;
+  const bool mine = row < rows;
+  const long token = t0 + (mine ? row : 0);
+  const int n = (int)(token % pb.N), b = (int)(token / pb.N);
+  const Place place(pb, b, n);
+  float2 w[E];   // cosine; sine, negative for the first member of a pair
+  int other[E];  // byte offset of the partner in a buffer
+  int turned = 0;  // channels of the chunk that turn (the first ones)
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = first + i;
+    other[i] = 0;
+    w[i] = make_float2(1.f, 0.f);
+    if (c >= pb.rot) continue;
+    turned = i + 1;
+    const Section s(pb, place, c);
+    const int r = c - s.start;
+    const bool lead = r < s.half;
+    const int at = row * pb.d + (lead ? c + s.half : c - s.half), chunk = at / E, in = at % E;
+    other[i] = ((in / kPerWord) * 32 + chunk) * 4 + in % kPerWord * (int)sizeof(T);
+    w[i] = turn(pb, s.start / 2 + (lead ? r : r - s.half), s.position);
+    if (lead) w[i].y = -w[i].y;
+  }
+  auto turn_chunk = [&](Chunk<T, E>& x, const uint32_t (*stage)[32]) {
+    const char* base = reinterpret_cast<const char*>(stage);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float a = to_f32(x.x[i]), e = to_f32(*reinterpret_cast<const T*>(base + other[i]));
+      if (i < turned) x.x[i] = from_f32<T>(fmaf(e, w[i].y, a * w[i].x));
+    }
   };
-  // this lane's chunks and pairs
-  int at[kPairs], to[kPairs];
-  float2 w[kPairs];
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const int x = i * 32 + lane, row = x / row_pairs;
-    at[i] = -1;
-    if (row >= rows) continue;
-    int axis = 0, start = 0, r = x % row_pairs;
-    while (r >= pb.dims[axis] / 2) {
-      r -= pb.dims[axis] / 2;
-      start += pb.dims[axis++];
-    }
-    int b;
-    const int n = place(row, &b);
-    at[i] = row * pb.d + start + r;
-    to[i] = at[i] + pb.dims[axis] / 2;
-    w[i] = turn(pb, start / 2 + r, token_position(pb, b, n, axis));
-  }
-  long src[2][2], dst[2][2];  // element offsets of the chunks in q and k (-1: none)
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int x = c * 32 + lane, row = x / row_chunks;
-    int b;
-    const int n = place(min(row, rows - 1), &b);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      src[t][c] = row < rows ? b * pb.in[t].b + n * pb.in[t].n + x % row_chunks * E : -1;
-      dst[t][c] = b * pb.out[t].b + n * pb.out[t].n + x % row_chunks * E;
-    }
-  }
-  const bool two = rows * row_chunks > 32;  // uniform: rows of more than 32 chunks
   const int h0 = blockIdx.y * sh.heads, h1 = min(h0 + sh.heads, pb.H[0] + pb.H[1]);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int lo = max(h0 - (t ? pb.H[0] : 0), 0), hi = min(h1 - (t ? pb.H[0] : 0), pb.H[t]);
-    const T* in = t ? k : q;
-    T* out = t ? ko : qo;
+    const T* src = (t ? k : q) + b * pb.in[t].b + n * pb.in[t].n + lo * pb.in[t].h + first;
+    T* dst = (t ? ko : qo) + b * pb.out[t].b + n * pb.out[t].n + lo * pb.out[t].h + first;
     for (int h = lo; h < hi; h += kBatch) {
       Chunk<T, E> x[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (h + i < hi && src[t][0] >= 0) read(x[i], in + src[t][0] + (h + i) * pb.in[t].h);
+        if (mine && h + i < hi) read(x[i], src + i * pb.in[t].h);
+      __syncwarp();  // the batch before is read
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (h + i < hi) {
-          if (src[t][0] >= 0) buf[warp][i][lane] = x[i];
-          if (two && src[t][1] >= 0) {
-            read(x[i], in + src[t][1] + (h + i) * pb.in[t].h);
-            buf[warp][i][32 + lane] = x[i];
-          }
+        if (mine && h + i < hi) {
+          const uint32_t* word = reinterpret_cast<const uint32_t*>(x[i].x);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) buf[warp][i][y][lane] = word[y];
         }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (h + i < hi) {
-          T* row = buf[warp][i][0].x;
-#pragma unroll
-          for (int p = 0; p < kPairs; ++p)
-            if (at[p] >= 0) {
-              const float a = to_f32(row[at[p]]), e = to_f32(row[to[p]]);
-              row[at[p]] = from_f32<T>(a * w[p].x - e * w[p].y);
-              row[to[p]] = from_f32<T>(e * w[p].x + a * w[p].y);
-            }
+        if (mine && h + i < hi) {
+          turn_chunk(x[i], buf[warp][i]);
+          write(x[i], dst + i * pb.out[t].h);
         }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (h + i < hi) {
-          if (src[t][0] >= 0)
-            write(buf[warp][i][lane], out + dst[t][0] + (h + i) * pb.out[t].h);
-          if (two && src[t][1] >= 0)
-            write(buf[warp][i][32 + lane], out + dst[t][1] + (h + i) * pb.out[t].h);
-        }
-      __syncwarp();
+      src += kBatch * pb.in[t].h;
+      dst += kBatch * pb.out[t].h;
     }
   }
 }
@@ -293,7 +302,8 @@ template <typename T>
 cudaError_t launch_staged(const T* const in[2], T* const out[2], const RotaryProblem& pb,
                           cudaStream_t stream, int* launches) {
   Shape sh = {};
-  sh.tokens = std::max(1, 32 / (pb.d / (16 / (int)sizeof(T))));  // of a warp
+  sh.units = pb.d / (16 / (int)sizeof(T));  // chunks of a token, at most 32
+  sh.tokens = 32 / sh.units;                // of a warp
   const dim3 grid = grid_of(pb, sh.tokens * (kThreads / 32), &sh);
   return timed_launch("rotary_staged", stream, launches, [&] {
     rotary_staged_kernel<T><<<grid, kThreads, 0, stream>>>(in[0], in[1], out[0], out[1], pb, sh);
@@ -320,7 +330,7 @@ cudaError_t rotary_forward(const T* const in[2], T* const out[2], const RotaryPr
   if (chunks && halves)
     return launch<T, Unit::kHalves>(in, out, pb, pb.rot / (2 * E) + (pb.d - pb.rot) / E, stream,
                                     launches);
-  if (chunks) return launch_staged<T>(in, out, pb, stream, launches);
+  if (chunks && pb.d <= 32 * E) return launch_staged<T>(in, out, pb, stream, launches);
   return launch<T, Unit::kPairs>(in, out, pb, pb.rot / 2 + pb.d - pb.rot, stream, launches);
 }
 
