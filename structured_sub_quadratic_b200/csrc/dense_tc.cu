@@ -28,9 +28,41 @@ __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
     if (global_ns() - t0 > kWaitLimitNs) break;
 }
 
+// One arrival for the warp, after the tcgen05 loads and stores of its lanes
+// (an arrival per thread would queue 32 updates of one word in shared memory,
+// whose bandwidth the products need).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // 16-byte unit u (channels 8u ..) of row r of a tile of swizzled 64-channel chunks.
 __device__ __forceinline__ uint4* row_unit(uint8_t* tile, int r, int u) {
   return reinterpret_cast<uint4*>(tile + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+}
+
+// 2^x of a pair on the FMA pipe, beside the exponential unit (16 results a
+// clock and SM, half of what the products of a d = 64 tile leave time for):
+// x = n + f with n the nearest integer (x + 1.5 2^23 has it in its low bits),
+// 2^f by the polynomial of least relative error on [-1/2, 1/2] (degree 5, by
+// Remez exchange: 7e-8, 2e-7 in fp32, as the unit's), n added to the exponent.
+// Below 2^-127 (hidden keys at -inf) the result is some value under 2^-125.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  x.x = fmaxf(x.x, -127.f);
+  x.y = fmaxf(x.y, -127.f);
+  const float2 big = make_float2(12582912.f, 12582912.f);
+  const float2 y = add2(x, big);
+  const float2 n = add2(y, make_float2(-12582912.f, -12582912.f));
+  const float2 f = add2(x, make_float2(-n.x, -n.y));
+  auto both = [](float c) { return make_float2(c, c); };
+  float2 p = fma2(both(1.3276472454890609e-3f), f, both(9.675540961325169e-3f));
+  p = fma2(p, f, both(5.550713092088699e-2f));
+  p = fma2(p, f, both(2.4022120237350464e-1f));
+  p = fma2(p, f, both(6.931469440460205e-1f));
+  p = fma2(p, f, both(1.0000001192092896f));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(y.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(y.y) << 23)));
 }
 
 // One 128-row tile of a (B, H, N, d) tensor, D channels: D / 64 boxes.  A
@@ -48,35 +80,53 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const TileMap& m, uint64
     tma_load_4d(dst + c * kChunk, &m.map, bar, c * 64, row, h * m.h_mul, b * m.b_mul);
 }
 
+// The products below are issued by a whole warp (one lane elected).
+
+// Wait of the whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
+__device__ __forceinline__ void warp_commit(uint64_t* bar) {
+  if (elect_one()) mma_commit(bar);
+}
+
 // D[tmem] (+)= A B^T over D channels, both tiles K-major in shared memory.
 template <int D>
 __device__ __forceinline__ void mma_nt(uint32_t tmem, uint64_t a, uint64_t b) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((kk >> 2) * kChunk + (kk & 3) * 32) >> 4;
-    mma_bf16_ss(tmem, a + off, b + off, idesc_bf16(kTile, kTile, false), kk > 0 ? 1u : 0u);
+    if (elect_one())
+      mma_bf16_ss(tmem, a + off, b + off, idesc_bf16(kTile, kTile, false), kk > 0 ? 1u : 0u);
   }
 }
 
-// D[tmem] (+)= W X: W 128 x 128 bf16 in TMEM, X a tile of 128 rows x D channels.
+// D[tmem] (+)= W X over half of X's rows (64 half ..): W 128 x 64 bf16 in
+// TMEM, X a tile of 128 rows x D channels.
 template <int D>
-__device__ __forceinline__ void mma_ts(uint32_t tmem, uint32_t w_tmem, uint64_t x,
-                                       bool accumulate) {
+__device__ __forceinline__ void mma_ts_half(uint32_t tmem, uint32_t w_tmem, uint64_t x, int half,
+                                            bool accumulate) {
 #pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_bf16_ts(tmem, w_tmem + kk * 8, x + ((kk * 16 * 128) >> 4), idesc_bf16(kTile, D, true),
+  for (int i = 0; i < kTile / 32; ++i) {
+    const int kk = half * (kTile / 32) + i;
+    if (elect_one())
+      mma_bf16_ts(tmem, w_tmem + i * 8, x + ((kk * 16 * 128) >> 4), idesc_bf16(kTile, D, true),
                 accumulate || kk > 0 ? 1u : 0u);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Forward.  One CTA per 256 queries of a head: two 128-row tiles whose
-// softmaxes (one warpgroup each, a thread per row) and products alternate, so
-// that one tile's S = Q K^T and O += P V run while the other's exponentials
-// do.  One pass over the keys: O stays in TMEM under a running maximum that
+// softmaxes (eight warps each, two threads per row with 64 keys of it) and
+// products alternate, so that one tile's S = Q K^T and O += P V run while the
+// other's exponentials do.  One pass over the keys: O stays in TMEM under a running maximum that
 // only moves when it grows by more than 2^8 (probabilities then reach 256,
 // exact in the bf16 of P as well as in the fp32 sum), so rescaling O is rare.
 // P overwrites S in TMEM and is the A operand of P V.
-// Warps: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA, 9 MMA.
+// Warps: 0-7 and 8-15 softmax of tile 0 and 1 (the first four of each have
+// keys 0-63 of a tile), 16 TMA, 17 MMA.
 // ---------------------------------------------------------------------------
 template <int D>
 struct FwdLayout {
@@ -85,9 +135,18 @@ struct FwdLayout {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr int kRowOff = kVOff + kStages * kTileBytes;  // float [2][2][2][128]
+  static constexpr int kBarOff = kRowOff + 8 * kTile * 4;
   static constexpr int kBytes = kBarOff + 32 * 8;
-  static constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S 0, S 1, then O 0, O 1
+  // TMEM columns: S 0, S 1; then O 0, O 1 with each half of P over the last
+  // 32 columns of its half of S (d > 64), or P 0, P 1, O 0, O 1, which lets the next S start as soon as
+  // this one is in registers.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kTmemCols = 512, kPCol = kOwnP ? 256 : 32;
+  static constexpr uint32_t kPStep = kOwnP ? 64 : 128, kOCol = kOwnP ? 384 : 256;
+  static constexpr uint32_t kPHalf = kOwnP ? 32 : 64;  // columns between the halves of P
+  // of 16 pairs of exponentials, those on the FMA pipe
+  static constexpr int kFmaPairs = D == 64 ? 6 : 4;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -98,7 +157,7 @@ struct FwdArgs {
   int* status;
 };
 
-constexpr int kFwdThreads = 320;
+constexpr int kFwdThreads = 576;
 
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -107,7 +166,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         const __grid_constant__ FwdArgs a) {
   using L = FwdLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // swizzled tiles need 1024-B alignment: report, never fault
     if (tid == 0) atomicExch(a.status, 2);
     return;
@@ -140,21 +199,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* q_full = bars;         // [2]
   uint64_t* s_full = bars + 2;     // [2]
-  uint64_t* p_full = bars + 4;     // [2]
-  uint64_t* o_full = bars + 6;     // [2]
-  uint64_t* k_full = bars + 8;     // [stages]
-  uint64_t* k_empty = bars + 11;
-  uint64_t* v_full = bars + 14;
-  uint64_t* v_empty = bars + 17;
-  uint64_t* v_tail = bars + 20;
-  uint64_t* drain = bars + 21;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 23);
+  uint64_t* s_read = bars + 4;     // [2], kOwnP
+  uint64_t* p_full = bars + 6;     // [2]
+  uint64_t* o_full = bars + 10;    // [2]: P V done (kOwnP: of every tile; else the last)
+  uint64_t* k_full = bars + 12;    // [stages]
+  uint64_t* k_empty = bars + 15;
+  uint64_t* v_full = bars + 18;
+  uint64_t* v_empty = bars + 21;
+  uint64_t* v_tail = bars + 24;
+  uint64_t* drain = bars + 25;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 27);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full + t, 1);
       mbar_init(s_full + t, 1);
-      mbar_init(p_full + t, kTile);
+      mbar_init(s_read + t, 8);
+      mbar_init(p_full + t, 8);
       mbar_init(o_full + t, 1);
     }
     for (int s = 0; s < L::kStages; ++s) {
@@ -168,16 +229,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---- TMA: Q, then K and V tile by tile ----
     bool ok = true;
     int kt = 0, vt = 0;  // tiles issued
@@ -225,62 +286,78 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (vt > s) drain_bar(v_full + s, ((vt - 1 - s) / L::kStages) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---- MMA issue ----
-    if (lane == 0 && n > 0) {
-      uint64_t dq[2], dk[L::kStages], dv[L::kStages];
+    if (n > 0) {
+      const uint64_t dq = desc_kmajor(smem_u32(smem + L::kQOff));
+      const uint64_t dk = desc_kmajor(smem_u32(smem + L::kKOff));
+      const uint64_t dv = desc_mnmajor(smem_u32(smem + L::kVOff), kChunk);
+      constexpr uint64_t kStep = L::kTileBytes >> 4;
+      bool ok = warp_wait(k_full, 0, abort_flag, a.status);
+#pragma unroll
       for (int t = 0; t < 2; ++t)
-        dq[t] = desc_kmajor(smem_u32(smem + L::kQOff + t * L::kTileBytes));
-      for (int s = 0; s < L::kStages; ++s) {
-        dk[s] = desc_kmajor(smem_u32(smem + L::kKOff + s * L::kTileBytes));
-        dv[s] = desc_mnmajor(smem_u32(smem + L::kVOff + s * L::kTileBytes), kChunk);
-      }
-      bool ok = mbar_wait(k_full, 0, abort_flag, a.status);
-      for (int t = 0; t < 2 && ok; ++t)
-        if (nt[t] > 0 && (ok = mbar_wait(q_full + t, 0, abort_flag, a.status))) {
-          mma_nt<D>(tmem + t * kTile, dq[t], dk[0]);
-          mma_commit(s_full + t);
+        if (ok && nt[t] > 0 && (ok = warp_wait(q_full + t, 0, abort_flag, a.status))) {
+          mma_nt<D>(tmem + t * kTile, dq + t * kStep, dk);
+          warp_commit(s_full + t);
         }
-      if (ok) mma_commit(k_empty);
+      if (ok) warp_commit(k_empty);
       int st = 0, ph = 0;  // stage and phase of tile j
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const int s1 = st + 1 == L::kStages ? 0 : st + 1, ph1 = s1 ? ph : ph ^ 1;
-        ok = mbar_wait(v_full + st, ph, abort_flag, a.status) &&
-             (j + 1 < n || tail == kTile || mbar_wait(v_tail, 0, abort_flag, a.status));
+        if (j + 1 < n && !(ok = warp_wait(k_full + s1, ph1, abort_flag, a.status))) break;
+        if (L::kOwnP) {  // the next S as soon as this one is in registers
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (ok && j + 1 < nt[t] && (ok = warp_wait(s_read + t, j & 1, abort_flag, a.status))) {
+              tc_fence_after();
+              mma_nt<D>(tmem + t * kTile, dq + t * kStep, dk + s1 * kStep);
+              warp_commit(s_full + t);
+            }
+          if (!ok) break;
+          if (j + 1 < n) warp_commit(k_empty + s1);
+        }
+        if (!(ok = warp_wait(v_full + st, ph, abort_flag, a.status))) break;
+        if (j + 1 == n && tail < kTile && !(ok = warp_wait(v_tail, 0, abort_flag, a.status))) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= nt[t]) continue;
-          if (!(ok = mbar_wait(p_full + t, j & 1, abort_flag, a.status))) continue;
+          if (!ok || j >= nt[t] || !(ok = warp_wait(p_full + t, j & 1, abort_flag, a.status)))
+            continue;
           tc_fence_after();
-          mma_ts<D>(tmem + L::kOCol + t * D, tmem + t * kTile, dv[st], j > 0);
-          if (j + 1 < nt[t]) {
-            // the products of one thread run in order: S overwrites P once P V has read it
-            if (!(ok = mbar_wait(k_full + s1, ph1, abort_flag, a.status))) continue;
-            mma_nt<D>(tmem + t * kTile, dq[t], dk[s1]);
-            mma_commit(s_full + t);  // also: P V of tile j is done
-          } else {
-            mma_commit(o_full + t);
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            mma_ts_half<D>(tmem + L::kOCol + t * D,
+                           tmem + L::kPCol + t * L::kPStep + y * L::kPHalf, dv + st * kStep, y,
+                           j > 0);
+          if (L::kOwnP || j + 1 == nt[t]) warp_commit(o_full + t);
+          if (!L::kOwnP && j + 1 < nt[t]) {
+            // the products of one thread run in order, so S overwrites P once
+            // P V has read it (and s_full says that P V is done, too)
+            mma_nt<D>(tmem + t * kTile, dq + t * kStep, dk + s1 * kStep);
+            warp_commit(s_full + t);
           }
         }
-        if (ok) {
-          mma_commit(v_empty + st);
-          if (j + 1 < n) mma_commit(k_empty + s1);
-        }
+        if (!ok) break;
+        warp_commit(v_empty + st);
+        if (!L::kOwnP && j + 1 < n) warp_commit(k_empty + s1);
         st = s1;
         ph = ph1;
       }
-      if (*abort_flag) {
-        mma_commit(drain);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+        warp_commit(drain);
         drain_bar(drain, 0);
       }
     }
   } else {
-    // ---- softmax: thread = row r of tile t ----
-    const int t = warp >> 2, r = tid & (kTile - 1);
+    // ---- softmax: thread = 64 keys of row r of tile t ----
+    const int t = warp >> 3, half = (warp >> 2) & 1, r = tid & (kTile - 1);
     const int r0 = q0 + t * kTile, row = r0 + r;
-    const int nj = nt[t];
+    const int nj = nt[t], pair = 1 + t * 4 + (warp & 3);  // barrier of the row's two warps
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + t * kTile + lane_off, to = tmem + L::kOCol + t * D + lane_off;
+    const uint32_t ts = tmem + t * kTile + half * 64 + lane_off;
+    const uint32_t tp = tmem + L::kPCol + t * L::kPStep + half * L::kPHalf + lane_off;
+    const uint32_t to = tmem + L::kOCol + t * D + half * (D / 2) + lane_off;
+    float* rows = reinterpret_cast<float*>(smem + L::kRowOff) + t * 4 * kTile + r;  // [2][2]
     const int vis = dense_visible(pb, len, row);
     const int all = dense_visible(pb, len, r0);  // keys that every row of the tile sees
     const float sl = pb.scale * kLog2e;
@@ -289,34 +366,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (int j = 0; j < nj; ++j) {
       if (!(ok = mbar_wait(s_full + t, j & 1, abort_flag, a.status))) break;
       tc_fence_after();
-      float s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
-      tmem_wait_ld();
-      if ((j + 1) * kTile > all) {
-        const int lim = vis - j * kTile;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+      // 32 keys at a time (96 registers a thread): both for the maximum, the
+      // second stays for its exponentials, the first is read again
+      float s[32], mx[4];
+      const bool masked = (j + 1) * kTile > all;
+      const int lim = vis - j * kTile - half * 64;
+      auto load_keys = [&](int c) {
+        tmem_ld32(ts + c * 32, s);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= lim) s[c][e] = -INFINITY;
-      }
-      float mx[4];
+            if (c * 32 + e >= lim) s[e] = -INFINITY;
+        }
+      };
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        mx[c] = fmaxf(s[c][0], s[c][1]);
+      for (int c = 0; c < 2; ++c) {
+        load_keys(c);
 #pragma unroll
-        for (int e = 2; e < 32; e += 2) mx[c] = max3(mx[c], s[c][e], s[c][e + 1]);
+        for (int y = 0; y < 2; ++y) {
+          const float* x = s + y * 16;
+          float v = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int e = 2; e < 16; e += 2) v = max3(v, x[e], x[e + 1]);
+          mx[2 * c + y] = v;
+        }
       }
-      const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      const float own = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+      rows[((j & 1) * 2 + half) * kTile] = own;
+      named_barrier(pair, 64);
+      const float mn = max3(m, own, rows[((j & 1) * 2 + (half ^ 1)) * kTile]);
+      if (L::kOwnP && j > 0) {  // O and P of the tile before are free
+        if (!(ok = mbar_wait(o_full + t, (j - 1) & 1, abort_flag, a.status))) break;
+        tc_fence_after();
+      }
       if (j == 0) {
         m = mn;
-      } else if (__any_sync(0xffffffffu, (mn - m) * sl > 8.f)) {
+      } else if (__any_sync(0xffffffffu, (mn - m) * sl > 8.f)) {  // the same in both warps
         const float f = m == mn ? 1.f : ex2((m - mn) * sl);
         z *= f;
         m = mn;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           float o[32];
           tmem_ld32(to + c * 32, o);
           tmem_wait_ld();
@@ -327,36 +418,47 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const float base = m == -INFINITY ? 0.f : -m * sl;
       const float2 sl2 = make_float2(sl, sl), base2 = make_float2(base, base);
-      float2 zs = make_float2(0.f, 0.f);
+      float2 zs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 1; c >= 0; --c) {
+        if (c == 0) {
+          load_keys(0);
+          if (L::kOwnP) {
+            warp_arrive(s_read + t);
+          }
+        }
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float2 x = fma2(make_float2(s[c][e], s[c][e + 1]), sl2, base2);
-          x.x = ex2(x.x);
-          x.y = ex2(x.y);
-          zs = add2(zs, x);
-          pk[e / 2] = pack_bf16x2(x.x, x.y);
+        for (int e = 0; e < 16; ++e) {
+          float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), sl2, base2);
+          if ((e + 1) * L::kFmaPairs / 16 > e * L::kFmaPairs / 16)  // spread over the 16
+            x = exp2_fma(x);
+          else
+            x = make_float2(ex2(x.x), ex2(x.y));
+          zs[e & 1] = add2(zs[e & 1], x);
+          pk[e] = pack_bf16x2(x.x, x.y);
         }
-        tmem_st16(ts + c * 16, pk);
+        tmem_st16(tp + c * 16, pk);
       }
-      z += zs.x + zs.y;
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full + t);
+      warp_arrive(p_full + t);
+      const float2 zz = add2(zs[0], zs[1]);
+      z += zz.x + zz.y;
     }
     if (r0 < pb.Nq) {
       // O / z to the tile of Q (read by every S of the tile), then one TMA store
       uint8_t* so = smem + L::kQOff + t * L::kTileBytes;
       if (ok) ok = mbar_wait(q_full + t, 0, abort_flag, a.status);
-      if (ok && nj > 0) ok = mbar_wait(o_full + t, 0, abort_flag, a.status);
+      if (ok && nj > 0)
+        ok = mbar_wait(o_full + t, L::kOwnP ? (nj - 1) & 1 : 0, abort_flag, a.status);
       tc_fence_after();
+      rows[((nj & 1) * 2 + half) * kTile] = z;
+      named_barrier(pair, 64);
       const bool any = vis > 0;
-      const float inv = 1.f / z;
+      const float sum = z + rows[((nj & 1) * 2 + (half ^ 1)) * kTile], inv = 1.f / sum;
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           float o[32];
           if (nj > 0) {
             tmem_ld32(to + c * 32, o);
@@ -366,19 +468,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * inv : 0.f;
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            *row_unit(so, r, c * 4 + u) =
+            *row_unit(so, r, half * (D / 16) + c * 4 + u) =
                 make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]),
                            pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
                            pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
                            pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
         }
-        if (row < pb.Nq)
+        if (half == 0 && row < pb.Nq)
           a.lse[((long)b * pb.H + h) * pb.Nq + row] =
-              any ? (m * sl + log2f(z)) * kLn2 : -INFINITY;
+              any ? (m * sl + log2f(sum)) * kLn2 : -INFINITY;
         fence_proxy_async_smem();
       }
-      named_barrier(1 + t, kTile);
-      if (r == 0 && ok && !*abort_flag) {
+      named_barrier(9 + t, 2 * kTile);
+      if (half == 0 && r == 0 && ok && !*abort_flag) {
         for (int c = 0; c < L::kCh; ++c)
           if (c * 64 < pb.d) tma_store_4d(&mo.map, so + c * kChunk, c * 64, r0, h, b);
         bulk_commit();
@@ -388,7 +490,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
@@ -438,7 +540,8 @@ __device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t w, uint64_t x
                                            bool accumulate) {
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_bf16_ts(tmem, w + (kk >> 2) * 64 + (kk & 3) * 8, x + ((kk * 16 * 128) >> 4),
+    if (elect_one())
+      mma_bf16_ts(tmem, w + (kk >> 2) * 64 + (kk & 3) * 8, x + ((kk * 16 * 128) >> 4),
                 idesc_bf16(kTile, D, true), accumulate || kk > 0 ? 1u : 0u);
 }
 
@@ -495,7 +598,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         const __grid_constant__ BwdArgs a) {
   using L = BwdLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (smem_u32(smem) & 1023u) {
     if (tid == 0) atomicExch(a.status, 2);
     return;
@@ -534,8 +637,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 2 * kTile);
-    mbar_init(ds_full, 2 * kTile);
+    mbar_init(p_full, 8);
+    mbar_init(ds_full, 8);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -547,7 +650,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 8) {
     // ---- TMA: K and V, then Q and dO tile by tile with lse and delta ----
@@ -591,45 +694,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 9) {
     // ---- MMA issue ----
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       const uint64_t dk = desc_kmajor(smem_u32(smem + L::kAOff));
       const uint64_t dv = desc_kmajor(smem_u32(smem + L::kBOff));
-      const uint32_t sx = smem_u32(smem + L::kXOff), sy = smem_u32(smem + L::kYOff);
-      bool ok = mbar_wait(kv_full, 0, abort_flag, a.status) &&
-                mbar_wait(q_full, 0, abort_flag, a.status);
+      const uint64_t xk = desc_kmajor(smem_u32(smem + L::kXOff));
+      const uint64_t yk = desc_kmajor(smem_u32(smem + L::kYOff));
+      const uint64_t xm = desc_mnmajor(smem_u32(smem + L::kXOff), kChunk);
+      const uint64_t ym = desc_mnmajor(smem_u32(smem + L::kYOff), kChunk);
+      constexpr uint64_t kStep = L::kTileBytes >> 4;
+      bool ok = warp_wait(kv_full, 0, abort_flag, a.status) &&
+                warp_wait(q_full, 0, abort_flag, a.status);
       if (ok) {
-        mma_nt<D>(tmem, dk, desc_kmajor(sx));
-        mma_commit(s_full);
-        ok = mbar_wait(g_full, 0, abort_flag, a.status);
+        mma_nt<D>(tmem, dk, xk);
+        warp_commit(s_full);
+        ok = warp_wait(g_full, 0, abort_flag, a.status);
       }
       if (ok) {
-        mma_nt<D>(tmem + L::kDPCol, dv, desc_kmajor(sy));
-        mma_commit(dp_full);
+        mma_nt<D>(tmem + L::kDPCol, dv, yk);
+        warp_commit(dp_full);
       }
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
-        const uint32_t x = sx + (i & 1) * L::kTileBytes, y = sy + (i & 1) * L::kTileBytes;
-        const uint32_t x1 = sx + (~i & 1) * L::kTileBytes, y1 = sy + (~i & 1) * L::kTileBytes;
+        const int st = i & 1, s1 = st ^ 1;
         const uint32_t ph1 = ((i + 1) >> 1) & 1;
-        if (!(ok = mbar_wait(p_full, i & 1, abort_flag, a.status))) break;
+        const bool more = i + 1 < n;
+        if (more && !(ok = warp_wait(q_full + s1, ph1, abort_flag, a.status))) break;
+        if (!(ok = warp_wait(p_full, i & 1, abort_flag, a.status))) break;
         tc_fence_after();
-        mma_halves<D>(tmem + L::kAccCol, tmem, desc_mnmajor(y, kChunk), i > 0);
-        if (i + 1 < n) {  // (in order: over P once dV has read it)
-          if (!(ok = mbar_wait(q_full + (~i & 1), ph1, abort_flag, a.status))) break;
-          mma_nt<D>(tmem, dk, desc_kmajor(x1));
-          mma_commit(s_full);
+        mma_halves<D>(tmem + L::kAccCol, tmem, ym + st * kStep, i > 0);
+        if (more) {  // (in order: over P once dV has read it)
+          mma_nt<D>(tmem, dk, xk + s1 * kStep);
+          warp_commit(s_full);
+          if (!(ok = warp_wait(g_full + s1, ph1, abort_flag, a.status))) break;
         }
-        if (!(ok = mbar_wait(ds_full, i & 1, abort_flag, a.status))) break;
+        if (!(ok = warp_wait(ds_full, i & 1, abort_flag, a.status))) break;
         tc_fence_after();
-        mma_halves<D>(tmem + L::kAccCol + D, tmem + L::kDPCol, desc_mnmajor(x, kChunk), i > 0);
-        mma_commit(empty + (i & 1));
-        if (i + 1 < n) {
-          if (!(ok = mbar_wait(g_full + (~i & 1), ph1, abort_flag, a.status))) break;
-          mma_nt<D>(tmem + L::kDPCol, dv, desc_kmajor(y1));
-          mma_commit(dp_full);
+        mma_halves<D>(tmem + L::kAccCol + D, tmem + L::kDPCol, xm + st * kStep, i > 0);
+        warp_commit(empty + st);
+        if (more) {
+          mma_nt<D>(tmem + L::kDPCol, dv, yk + s1 * kStep);
+          warp_commit(dp_full);
         }
       }
-      mma_commit(done);
-      if (*abort_flag) drain_bar(done, 0);
+      warp_commit(done);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) drain_bar(done, 0);
     }
   } else {
     // ---- thread = key r, 64 query columns ----
@@ -668,8 +776,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       store_half(ts, p);
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full);
+      warp_arrive(p_full);
       if (!(ok = mbar_wait(dp_full, i & 1, abort_flag, a.status))) break;
       tc_fence_after();
       float d[64];
@@ -689,8 +796,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       store_half(tp, d);
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(ds_full);
+      warp_arrive(ds_full);
     }
     if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
     tc_fence_after();
@@ -729,7 +835,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                        const __grid_constant__ TileMap mdq, const __grid_constant__ BwdArgs a) {
   using L = BwdLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (smem_u32(smem) & 1023u) {
     if (tid == 0) atomicExch(a.status, 2);
     return;
@@ -768,9 +874,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     mbar_init(k_tail, 1);
     mbar_init(s_full, 1);
-    mbar_init(s_read, 2 * kTile);
+    mbar_init(s_read, 8);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 2 * kTile);
+    mbar_init(ds_full, 8);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -782,7 +888,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 8) {
     // ---- TMA: Q and dO, then K and V tile by tile ----
@@ -828,47 +934,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 9) {
     // ---- MMA issue ----
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       const uint64_t dq = desc_kmajor(smem_u32(smem + L::kAOff));
       const uint64_t dg = desc_kmajor(smem_u32(smem + L::kBOff));
-      const uint32_t sx = smem_u32(smem + L::kXOff), sy = smem_u32(smem + L::kYOff);
+      const uint64_t xk = desc_kmajor(smem_u32(smem + L::kXOff));
+      const uint64_t yk = desc_kmajor(smem_u32(smem + L::kYOff));
+      const uint64_t xm = desc_mnmajor(smem_u32(smem + L::kXOff), kChunk);
+      constexpr uint64_t kStep = L::kTileBytes >> 4;
       auto key_tile = [&](int j) {
-        return mbar_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag, a.status) &&
-               (j + 1 < n || tail == kTile || mbar_wait(k_tail, 0, abort_flag, a.status));
+        return warp_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag, a.status) &&
+               (j + 1 < n || tail == kTile || warp_wait(k_tail, 0, abort_flag, a.status));
       };
-      bool ok = mbar_wait(qg_full, 0, abort_flag, a.status) && key_tile(0);
+      bool ok = warp_wait(qg_full, 0, abort_flag, a.status) && key_tile(0);
       if (ok) {
-        mma_nt<D>(tmem, dq, desc_kmajor(sx));
-        mma_commit(s_full);
-        ok = mbar_wait(v_full, 0, abort_flag, a.status);
+        mma_nt<D>(tmem, dq, xk);
+        warp_commit(s_full);
+        ok = warp_wait(v_full, 0, abort_flag, a.status);
       }
       if (ok) {
-        mma_nt<D>(tmem + L::kDPCol, dg, desc_kmajor(sy));
-        mma_commit(dp_full);
-        mma_commit(v_empty);
+        mma_nt<D>(tmem + L::kDPCol, dg, yk);
+        warp_commit(dp_full);
+        warp_commit(v_empty);
       }
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const int st = j & 1, s1 = st ^ 1;
-        if (j + 1 < n) {
-          if (!(ok = key_tile(j + 1) && mbar_wait(s_read, j & 1, abort_flag, a.status))) break;
+        const bool more = j + 1 < n;
+        if (more) {
+          if (!(ok = key_tile(j + 1) && warp_wait(s_read, j & 1, abort_flag, a.status))) break;
           tc_fence_after();
-          mma_nt<D>(tmem, dq, desc_kmajor(sx + s1 * L::kTileBytes));
-          mma_commit(s_full);
+          mma_nt<D>(tmem, dq, xk + s1 * kStep);
+          warp_commit(s_full);
+          if (!(ok = warp_wait(v_full + s1, ((j + 1) >> 1) & 1, abort_flag, a.status))) break;
         }
-        if (!(ok = mbar_wait(ds_full, j & 1, abort_flag, a.status))) break;
+        if (!(ok = warp_wait(ds_full, j & 1, abort_flag, a.status))) break;
         tc_fence_after();
-        mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol,
-                      desc_mnmajor(sx + st * L::kTileBytes, kChunk), j > 0);
-        mma_commit(k_empty + st);
-        if (j + 1 < n) {  // (in order: over dS once dQ has read it)
-          if (!(ok = mbar_wait(v_full + s1, ((j + 1) >> 1) & 1, abort_flag, a.status))) break;
-          mma_nt<D>(tmem + L::kDPCol, dg, desc_kmajor(sy + s1 * L::kTileBytes));
-          mma_commit(dp_full);
-          mma_commit(v_empty + s1);
+        mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol, xm + st * kStep, j > 0);
+        warp_commit(k_empty + st);
+        if (more) {  // (in order: over dS once dQ has read it)
+          mma_nt<D>(tmem + L::kDPCol, dg, yk + s1 * kStep);
+          warp_commit(dp_full);
+          warp_commit(v_empty + s1);
         }
       }
-      mma_commit(done);
-      if (*abort_flag) drain_bar(done, 0);
+      warp_commit(done);
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) drain_bar(done, 0);
     }
   } else {
     // ---- thread = query r, 64 key columns ----
@@ -889,8 +999,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       float p[64];
       load_half(ts, p);
-      tc_fence_before();
-      mbar_arrive(s_read);
+      warp_arrive(s_read);
 #pragma unroll
       for (int e = 0; e < 64; e += 2) {
         const float2 u = fma2(make_float2(p[e], p[e + 1]), sl2, base2);
@@ -916,8 +1025,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       store_half(tp, d);
       tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(ds_full);
+      warp_arrive(ds_full);
     }
     if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
     tc_fence_after();
