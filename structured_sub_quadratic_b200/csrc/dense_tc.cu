@@ -92,42 +92,78 @@ __device__ __forceinline__ void warp_commit(uint64_t* bar) {
   if (elect_one()) mma_commit(bar);
 }
 
-// D[tmem] (+)= A B^T over D channels, both tiles K-major in shared memory.
-template <int D>
+// D[tmem] = A B^T over D channels: A a tile, B a tile or its first N rows,
+// both K-major in shared memory.
+template <int D, int N = kTile>
 __device__ __forceinline__ void mma_nt(uint32_t tmem, uint64_t a, uint64_t b) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((kk >> 2) * kChunk + (kk & 3) * 32) >> 4;
     if (elect_one())
-      mma_bf16_ss(tmem, a + off, b + off, idesc_bf16(kTile, kTile, false), kk > 0 ? 1u : 0u);
+      mma_bf16_ss(tmem, a + off, b + off, idesc_bf16(kTile, N, false), kk > 0 ? 1u : 0u);
   }
 }
 
-// D[tmem] (+)= W X over half of X's rows (64 half ..): W 128 x 64 bf16 in
-// TMEM, X a tile of 128 rows x D channels.
+// D[tmem] (+)= W X: W 128 x 64 bf16 in TMEM, X 64 rows of a tile, D channels.
 template <int D>
-__device__ __forceinline__ void mma_ts_half(uint32_t tmem, uint32_t w_tmem, uint64_t x, int half,
-                                            bool accumulate) {
+__device__ __forceinline__ void mma_ts64(uint32_t tmem, uint32_t w_tmem, uint64_t x,
+                                         bool accumulate) {
 #pragma unroll
-  for (int i = 0; i < kTile / 32; ++i) {
-    const int kk = half * (kTile / 32) + i;
+  for (int kk = 0; kk < 4; ++kk)
     if (elect_one())
-      mma_bf16_ts(tmem, w_tmem + i * 8, x + ((kk * 16 * 128) >> 4), idesc_bf16(kTile, D, true),
-                accumulate || kk > 0 ? 1u : 0u);
+      mma_bf16_ts(tmem, w_tmem + kk * 8, x + ((kk * 16 * 128) >> 4), idesc_bf16(kTile, D, true),
+                  accumulate || kk > 0 ? 1u : 0u);
+}
+
+// 64 columns of this thread's lane.
+__device__ __forceinline__ void load_half(uint32_t taddr, float (&x)[64]) {
+  float t[2][32];
+  tmem_ld32(taddr, t[0]);
+  tmem_ld32(taddr + 32, t[1]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 64; ++e) x[e] = t[e >> 5][e & 31];
+}
+
+// Row r of a D-wide accumulator times `f`, as bf16, into a swizzled tile;
+// zeros where nothing was accumulated (the columns hold anything) or `keep`
+// is false.
+template <int D>
+__device__ __forceinline__ void accumulator_row(uint8_t* tile, int r, uint32_t taddr, float f,
+                                                bool any, bool keep = true) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    if (any) {
+      tmem_ld32(taddr + c * 32, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = any && keep ? o[e] * f : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *row_unit(tile, r, c * 4 + u) =
+          make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                     pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
+                     pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
   }
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  One CTA per 256 queries of a head: two 128-row tiles whose
-// softmaxes (eight warps each, two threads per row with 64 keys of it) and
-// products alternate, so that one tile's S = Q K^T and O += P V run while the
-// other's exponentials do.  One pass over the keys: O stays in TMEM under a running maximum that
-// only moves when it grows by more than 2^8 (probabilities then reach 256,
-// exact in the bf16 of P as well as in the fp32 sum), so rescaling O is rare.
-// P overwrites S in TMEM and is the A operand of P V.
-// Warps: 0-7 and 8-15 softmax of tile 0 and 1 (the first four of each have
-// keys 0-63 of a tile), 16 TMA, 17 MMA.
+// Forward.  One CTA per 256 queries of a head: two 128-row tiles, a warpgroup
+// each with a thread per row, walk the keys 64 at a time in one pass.  S has
+// two buffers a tile, so that S of step u + 2 is issued right behind P V of
+// step u and the softmaxes never wait for a product that has not long begun
+// (with one 128-key buffer, the chain softmax, P V, S took 3450 clocks per 256
+// x 128 scores at d = 128, against 2070 of products).  O stays in TMEM
+// under a running maximum that only moves when it grows by more than 2^8
+// (probabilities then reach 256, exact in the exponents of P's bf16 and of the
+// fp32 sum), so rescaling O is rare.  P overwrites S and is the A operand of
+// P V.
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1, 8 TMA, 9 MMA.
 // ---------------------------------------------------------------------------
+constexpr int kStep = 64;  // keys of a step
+
 template <int D>
 struct FwdLayout {
   static constexpr int kCh = D / 64, kStages = D == 128 ? 2 : 3;
@@ -135,18 +171,12 @@ struct FwdLayout {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kRowOff = kVOff + kStages * kTileBytes;  // float [2][2][2][128]
-  static constexpr int kBarOff = kRowOff + 8 * kTile * 4;
+  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
   static constexpr int kBytes = kBarOff + 32 * 8;
-  // TMEM columns: S 0, S 1; then O 0, O 1 with each half of P over the last
-  // 32 columns of its half of S (d > 64), or P 0, P 1, O 0, O 1, which lets the next S start as soon as
-  // this one is in registers.
-  static constexpr bool kOwnP = D == 64;
-  static constexpr uint32_t kTmemCols = 512, kPCol = kOwnP ? 256 : 32;
-  static constexpr uint32_t kPStep = kOwnP ? 64 : 128, kOCol = kOwnP ? 384 : 256;
-  static constexpr uint32_t kPHalf = kOwnP ? 32 : 64;  // columns between the halves of P
+  // TMEM columns: S of tile t and buffer y at 128 t + 64 y, O at 256 + D t
+  static constexpr uint32_t kTmemCols = 512, kOCol = 256;
   // of 16 pairs of exponentials, those on the FMA pipe
-  static constexpr int kFmaPairs = D == 64 ? 6 : 4;
+  static constexpr int kFmaPairs = 4;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -157,7 +187,7 @@ struct FwdArgs {
   int* status;
 };
 
-constexpr int kFwdThreads = 576;
+constexpr int kFwdThreads = 320;
 
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -184,39 +214,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int h = bh % pb.H, b = bh / pb.H, hk = h / (pb.H / pb.Hkv);
   const int q0 = tile * 2 * kTile;
   const int len = dense_len(pb, b);
-  // key tiles of the two row tiles, and the last one's rows past the length
+  // steps of the two row tiles, key tiles, and the last one's rows past the length
   int nt[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r0 = q0 + t * kTile;
     nt[t] = r0 < pb.Nq
-                ? (dense_visible(pb, len, min(r0 + kTile, pb.Nq) - 1) + kTile - 1) / kTile
+                ? (dense_visible(pb, len, min(r0 + kTile, pb.Nq) - 1) + kStep - 1) / kStep
                 : 0;
   }
-  const int n = max(nt[0], nt[1]);
+  const int steps = max(nt[0], nt[1]), n = (steps + 1) / 2;
   const int tail = n * kTile > len && len < pb.Nk ? len - (n - 1) * kTile : kTile;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-  uint64_t* q_full = bars;         // [2]
-  uint64_t* s_full = bars + 2;     // [2]
-  uint64_t* s_read = bars + 4;     // [2], kOwnP
-  uint64_t* p_full = bars + 6;     // [2]
-  uint64_t* o_full = bars + 10;    // [2]: P V done (kOwnP: of every tile; else the last)
-  uint64_t* k_full = bars + 12;    // [stages]
-  uint64_t* k_empty = bars + 15;
-  uint64_t* v_full = bars + 18;
-  uint64_t* v_empty = bars + 21;
-  uint64_t* v_tail = bars + 24;
-  uint64_t* drain = bars + 25;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 27);
+  uint64_t* q_full = bars;       // [2]
+  uint64_t* s_full = bars + 2;   // [2][2]: S of a step, and P V of the one two before
+  uint64_t* p_full = bars + 6;   // [2][2]: P of a step (a softmax may be one step ahead)
+  uint64_t* k_full = bars + 10;  // [stages]
+  uint64_t* k_empty = bars + 13;
+  uint64_t* v_full = bars + 16;
+  uint64_t* v_empty = bars + 19;
+  uint64_t* v_tail = bars + 22;
+  uint64_t* drain = bars + 23;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 25);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full + t, 1);
-      mbar_init(s_full + t, 1);
-      mbar_init(s_read + t, 8);
-      mbar_init(p_full + t, 8);
-      mbar_init(o_full + t, 1);
+      mbar_init(s_full + 2 * t, 1);
+      mbar_init(s_full + 2 * t + 1, 1);
+      mbar_init(p_full + 2 * t, 4);
+      mbar_init(p_full + 2 * t + 1, 4);
     }
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(k_full + s, 1);
@@ -229,7 +257,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 17) {
+  if (warp == 9) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
@@ -238,7 +266,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp == 16) {
+  if (warp == 8) {
     // ---- TMA: Q, then K and V tile by tile ----
     bool ok = true;
     int kt = 0, vt = 0;  // tiles issued
@@ -286,60 +314,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (vt > s) drain_bar(v_full + s, ((vt - 1 - s) / L::kStages) & 1);
       }
     }
-  } else if (warp == 17) {
+  } else if (warp == 9) {
     // ---- MMA issue ----
     if (n > 0) {
       const uint64_t dq = desc_kmajor(smem_u32(smem + L::kQOff));
       const uint64_t dk = desc_kmajor(smem_u32(smem + L::kKOff));
       const uint64_t dv = desc_mnmajor(smem_u32(smem + L::kVOff), kChunk);
-      constexpr uint64_t kStep = L::kTileBytes >> 4;
+      constexpr uint64_t kTileStep = L::kTileBytes >> 4, kHalf = (kStep * 128) >> 4;
+      auto issue_s = [&](int t, int y, int st) {
+        mma_nt<D, kStep>(tmem + t * kTile + y * kStep, dq + t * kTileStep,
+                         dk + st * kTileStep + y * kHalf);
+      };
       bool ok = warp_wait(k_full, 0, abort_flag, a.status);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (ok && nt[t] > 0 && (ok = warp_wait(q_full + t, 0, abort_flag, a.status))) {
-          mma_nt<D>(tmem + t * kTile, dq + t * kStep, dk);
-          warp_commit(s_full + t);
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (y < nt[t]) {
+              issue_s(t, y, 0);
+              warp_commit(s_full + 2 * t + y);
+            }
         }
       if (ok) warp_commit(k_empty);
-      int st = 0, ph = 0;  // stage and phase of tile j
+      int st = 0, ph = 0;  // stage and phase of key tile j
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const int s1 = st + 1 == L::kStages ? 0 : st + 1, ph1 = s1 ? ph : ph ^ 1;
-        if (j + 1 < n && !(ok = warp_wait(k_full + s1, ph1, abort_flag, a.status))) break;
-        if (L::kOwnP) {  // the next S as soon as this one is in registers
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (ok && j + 1 < nt[t] && (ok = warp_wait(s_read + t, j & 1, abort_flag, a.status))) {
-              tc_fence_after();
-              mma_nt<D>(tmem + t * kTile, dq + t * kStep, dk + s1 * kStep);
-              warp_commit(s_full + t);
-            }
-          if (!ok) break;
-          if (j + 1 < n) warp_commit(k_empty + s1);
-        }
         if (!(ok = warp_wait(v_full + st, ph, abort_flag, a.status))) break;
         if (j + 1 == n && tail < kTile && !(ok = warp_wait(v_tail, 0, abort_flag, a.status))) break;
+        if (j + 1 < n && !(ok = warp_wait(k_full + s1, ph1, abort_flag, a.status))) break;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= nt[t] || !(ok = warp_wait(p_full + t, j & 1, abort_flag, a.status)))
-            continue;
-          tc_fence_after();
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-            mma_ts_half<D>(tmem + L::kOCol + t * D,
-                           tmem + L::kPCol + t * L::kPStep + y * L::kPHalf, dv + st * kStep, y,
-                           j > 0);
-          if (L::kOwnP || j + 1 == nt[t]) warp_commit(o_full + t);
-          if (!L::kOwnP && j + 1 < nt[t]) {
+          for (int t = 0; t < 2; ++t) {
+            const int u = 2 * j + y;
+            if (!ok || u >= nt[t] || !(ok = warp_wait(p_full + 2 * t + y, j & 1, abort_flag, a.status)))
+              continue;
+            tc_fence_after();
+            mma_ts64<D>(tmem + L::kOCol + t * D, tmem + t * kTile + y * kStep,
+                        dv + st * kTileStep + y * kHalf, u > 0);
             // the products of one thread run in order, so S overwrites P once
-            // P V has read it (and s_full says that P V is done, too)
-            mma_nt<D>(tmem + t * kTile, dq + t * kStep, dk + s1 * kStep);
-            warp_commit(s_full + t);
+            // P V has read it
+            if (u + 2 < nt[t]) issue_s(t, y, s1);
+            warp_commit(s_full + 2 * t + y);
           }
-        }
         if (!ok) break;
         warp_commit(v_empty + st);
-        if (!L::kOwnP && j + 1 < n) warp_commit(k_empty + s1);
+        if (j + 1 < n) warp_commit(k_empty + s1);
         st = s1;
         ph = ph1;
       }
@@ -349,65 +371,51 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
     }
   } else {
-    // ---- softmax: thread = 64 keys of row r of tile t ----
-    const int t = warp >> 3, half = (warp >> 2) & 1, r = tid & (kTile - 1);
+    // ---- softmax: thread = row r of tile t ----
+    const int t = warp >> 2, r = tid & (kTile - 1);
     const int r0 = q0 + t * kTile, row = r0 + r;
-    const int nj = nt[t], pair = 1 + t * 4 + (warp & 3);  // barrier of the row's two warps
+    const int nj = nt[t];
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + t * kTile + half * 64 + lane_off;
-    const uint32_t tp = tmem + L::kPCol + t * L::kPStep + half * L::kPHalf + lane_off;
-    const uint32_t to = tmem + L::kOCol + t * D + half * (D / 2) + lane_off;
-    float* rows = reinterpret_cast<float*>(smem + L::kRowOff) + t * 4 * kTile + r;  // [2][2]
+    const uint32_t ts = tmem + t * kTile + lane_off, to = tmem + L::kOCol + t * D + lane_off;
     const int vis = dense_visible(pb, len, row);
     const int all = dense_visible(pb, len, r0);  // keys that every row of the tile sees
     const float sl = pb.scale * kLog2e;
+    const float2 sl2 = make_float2(sl, sl);
     float m = -INFINITY, z = 0.f;
     bool ok = true;
-    for (int j = 0; j < nj; ++j) {
-      if (!(ok = mbar_wait(s_full + t, j & 1, abort_flag, a.status))) break;
+#pragma unroll 1
+    for (int u = 0; u < nj; ++u) {
+      uint64_t* full = s_full + 2 * t + (u & 1);
+      if (!(ok = mbar_wait(full, (u >> 1) & 1, abort_flag, a.status))) break;
       tc_fence_after();
-      // 32 keys at a time (96 registers a thread): both for the maximum, the
-      // second stays for its exponentials, the first is read again
-      float s[32], mx[4];
-      const bool masked = (j + 1) * kTile > all;
-      const int lim = vis - j * kTile - half * 64;
-      auto load_keys = [&](int c) {
-        tmem_ld32(ts + c * 32, s);
-        tmem_wait_ld();
-        if (masked) {
+      float s[64];
+      load_half(ts + (u & 1) * kStep, s);
+      if ((u + 1) * kStep > all) {
+        const int lim = vis - u * kStep;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= lim) s[e] = -INFINITY;
-        }
-      };
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        load_keys(c);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float* x = s + y * 16;
-          float v = fmaxf(x[0], x[1]);
-#pragma unroll
-          for (int e = 2; e < 16; e += 2) v = max3(v, x[e], x[e + 1]);
-          mx[2 * c + y] = v;
-        }
+        for (int e = 0; e < 64; ++e)
+          if (e >= lim) s[e] = -INFINITY;
       }
-      const float own = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-      rows[((j & 1) * 2 + half) * kTile] = own;
-      named_barrier(pair, 64);
-      const float mn = max3(m, own, rows[((j & 1) * 2 + (half ^ 1)) * kTile]);
-      if (L::kOwnP && j > 0) {  // O and P of the tile before are free
-        if (!(ok = mbar_wait(o_full + t, (j - 1) & 1, abort_flag, a.status))) break;
-        tc_fence_after();
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = fmaxf(s[16 * c], s[16 * c + 1]);
+#pragma unroll
+        for (int e = 2; e < 16; e += 2) mx[c] = max3(mx[c], s[16 * c + e], s[16 * c + e + 1]);
       }
-      if (j == 0) {
+      const float mn = max3(max3(m, mx[0], mx[1]), mx[2], mx[3]);
+      if (u == 0) {
         m = mn;
-      } else if (__any_sync(0xffffffffu, (mn - m) * sl > 8.f)) {  // the same in both warps
+      } else if (__any_sync(0xffffffffu, (mn - m) * sl > 8.f)) {
+        // O as step u - 1 leaves it: its P V is behind the other buffer's next phase
+        if (!(ok = mbar_wait(s_full + 2 * t + (~u & 1), ((u + 1) >> 1) & 1, abort_flag, a.status)))
+          break;
+        tc_fence_after();
         const float f = m == mn ? 1.f : ex2((m - mn) * sl);
         z *= f;
         m = mn;
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           float o[32];
           tmem_ld32(to + c * 32, o);
           tmem_wait_ld();
@@ -417,20 +425,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       }
       const float base = m == -INFINITY ? 0.f : -m * sl;
-      const float2 sl2 = make_float2(sl, sl), base2 = make_float2(base, base);
+      const float2 base2 = make_float2(base, base);
       float2 zs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 1; c >= 0; --c) {
-        if (c == 0) {
-          load_keys(0);
-          if (L::kOwnP) {
-            warp_arrive(s_read + t);
-          }
-        }
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), sl2, base2);
+          float2 x = fma2(make_float2(s[c * 32 + 2 * e], s[c * 32 + 2 * e + 1]), sl2, base2);
           if ((e + 1) * L::kFmaPairs / 16 > e * L::kFmaPairs / 16)  // spread over the 16
             x = exp2_fma(x);
           else
@@ -438,10 +440,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           zs[e & 1] = add2(zs[e & 1], x);
           pk[e] = pack_bf16x2(x.x, x.y);
         }
-        tmem_st16(tp + c * 16, pk);
+        tmem_st16(ts + (u & 1) * kStep + c * 16, pk);
       }
       tmem_wait_st();
-      warp_arrive(p_full + t);
+      warp_arrive(p_full + 2 * t + (u & 1));
       const float2 zz = add2(zs[0], zs[1]);
       z += zz.x + zz.y;
     }
@@ -449,38 +451,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // O / z to the tile of Q (read by every S of the tile), then one TMA store
       uint8_t* so = smem + L::kQOff + t * L::kTileBytes;
       if (ok) ok = mbar_wait(q_full + t, 0, abort_flag, a.status);
-      if (ok && nj > 0)
-        ok = mbar_wait(o_full + t, L::kOwnP ? (nj - 1) & 1 : 0, abort_flag, a.status);
+      if (ok && nj > 0)  // P V of the last step
+        ok = mbar_wait(s_full + 2 * t + (~nj & 1), ((nj + 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
-      rows[((nj & 1) * 2 + half) * kTile] = z;
-      named_barrier(pair, 64);
       const bool any = vis > 0;
-      const float sum = z + rows[((nj & 1) * 2 + (half ^ 1)) * kTile], inv = 1.f / sum;
       if (ok) {
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          float o[32];
-          if (nj > 0) {
-            tmem_ld32(to + c * 32, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * inv : 0.f;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *row_unit(so, r, half * (D / 16) + c * 4 + u) =
-                make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]),
-                           pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                           pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
-                           pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-        }
-        if (half == 0 && row < pb.Nq)
+        accumulator_row<D>(so, r, to, 1.f / z, nj > 0, any);
+        if (row < pb.Nq)
           a.lse[((long)b * pb.H + h) * pb.Nq + row] =
-              any ? (m * sl + log2f(sum)) * kLn2 : -INFINITY;
+              any ? (m * sl + log2f(z)) * kLn2 : -INFINITY;
         fence_proxy_async_smem();
       }
-      named_barrier(9 + t, 2 * kTile);
-      if (half == 0 && r == 0 && ok && !*abort_flag) {
+      named_barrier(1 + t, kTile);
+      if (r == 0 && ok && !*abort_flag) {
         for (int c = 0; c < L::kCh; ++c)
           if (c * 64 < pb.d) tma_store_4d(&mo.map, so + c * kChunk, c * 64, r0, h, b);
         bulk_commit();
@@ -490,7 +473,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
@@ -525,15 +508,6 @@ __device__ __forceinline__ void store_half(uint32_t taddr, const float (&x)[64])
   }
 }
 
-__device__ __forceinline__ void load_half(uint32_t taddr, float (&x)[64]) {
-  float t[2][32];
-  tmem_ld32(taddr, t[0]);
-  tmem_ld32(taddr + 32, t[1]);
-  tmem_wait_ld();
-#pragma unroll
-  for (int e = 0; e < 64; ++e) x[e] = t[e >> 5][e & 31];
-}
-
 // D[tmem] (+)= W X, W's columns 0-63 and 64-127 as store_half left them.
 template <int D>
 __device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t w, uint64_t x,
@@ -543,28 +517,6 @@ __device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t w, uint64_t x
     if (elect_one())
       mma_bf16_ts(tmem, w + (kk >> 2) * 64 + (kk & 3) * 8, x + ((kk * 16 * 128) >> 4),
                 idesc_bf16(kTile, D, true), accumulate || kk > 0 ? 1u : 0u);
-}
-
-// Row r of a D-wide accumulator times `f`, as bf16, into a swizzled tile.
-template <int D>
-__device__ __forceinline__ void accumulator_row(uint8_t* tile, int r, uint32_t taddr, float f,
-                                                bool any) {
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    float o[32];
-    if (any) {
-      tmem_ld32(taddr + c * 32, o);
-      tmem_wait_ld();
-    }
-#pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * f : 0.f;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      *row_unit(tile, r, c * 4 + u) =
-          make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                     pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
-                     pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-  }
 }
 
 template <int D>
