@@ -3,23 +3,24 @@
 // tensor-core kernels do not take (d above 128 or not a multiple of 8,
 // unaligned rows).
 //
-// One 256-thread CTA owns a tile of BT rows (queries, or keys in the dK, dV
-// kernel) and walks the tiles of the other axis with both operands widened
-// to fp32 in shared memory.  Thread (ty, tx) of the 16 x 16 block holds rows
-// ty + 16 i and columns tx + 16 j of each score tile, and columns
-// 4 tx + 64 c of each d-wide accumulator.  Bound: the FFMA pipe, fed by
-// float4 shared loads (rows padded by 4 floats, conflict-free).
+// A CTA owns a tile of ROWS rows (queries, or keys in the dK, dV kernel) and
+// walks tiles of COLS of the other axis, both widened to fp32 in shared
+// memory.  Of its 4 ROWS threads, thread (ty, tx) holds rows ty + ROWS/4 i
+// (i < 4) and columns tx + 16 j of each score tile, and columns 4 tx + 64 c of
+// each d-wide accumulator.  Bound: the FFMA pipe, fed by float4 shared loads
+// (rows padded by 4 floats, conflict-free) in packed pairs of channels.
 #include "dense.cuh"
 
 #include <math.h>
 
 #include "launch.cuh"
+#include "tc_ptx.cuh"
 #include "timing.cuh"
 
 namespace monarch {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kDeltaThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -52,11 +53,11 @@ __device__ __forceinline__ void store4<bf16>(bf16* p, float4 v) {
 // Rows [r0, r0 + BT) of one head into shared memory as fp32, rows from n on
 // and channels from d on zero.  vec: rows allow four-element loads and
 // d % 4 == 0.
-template <typename T, int BT, int DP>
+template <typename T, int BT, int DP, int THREADS>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, long stride, int r0, int n,
                                           int d, bool vec) {
   constexpr int kPitch = DP + 4;
-  for (int x = threadIdx.x; x < BT * (DP / 4); x += kThreads) {
+  for (int x = threadIdx.x; x < BT * (DP / 4); x += THREADS) {
     const int r = x / (DP / 4), c = x % (DP / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + r < n && c < d) {
@@ -87,47 +88,51 @@ __device__ __forceinline__ void store_row4(T* p, float4 v, int c, int d, bool ve
   }
 }
 
-// acc[i][j] = A[ty + 16 i] . B[tx + 16 j] over DP channels.
-template <int BT, int DP>
+// acc[i][j] = A[ty + ROWS/4 i] . B[tx + 16 j] over DP channels; even and odd
+// channels are summed apart (one packed instruction for both).
+template <int ROWS, int COLS, int DP>
 __device__ __forceinline__ void scores(const float* A, const float* B, int ty, int tx,
-                                       float (&acc)[BT / 16][BT / 16]) {
-  constexpr int R = BT / 16, kPitch = DP + 4;
+                                       float (&acc)[4][COLS / 16]) {
+  constexpr int J = COLS / 16, kPitch = DP + 4;
+  float2 s[4][J];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < J; ++j) s[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int c = 0; c < DP; c += 4) {
-    float4 a[R], b[R];
+    float4 a[4], b[J];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPitch + c);
+    for (int i = 0; i < 4; ++i)
+      a[i] = *reinterpret_cast<const float4*>(A + (ty + ROWS / 4 * i) * kPitch + c);
 #pragma unroll
-    for (int j = 0; j < R; ++j)
+    for (int j = 0; j < J; ++j)
       b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * kPitch + c);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+      for (int j = 0; j < J; ++j) {
+        s[i][j] = tc::fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s[i][j]);
+        s[i][j] = tc::fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
 }
 
-// acc[i][c] += sum_k W[ty + 16 i][k] X[k][4 tx + 64 c ..].
-template <int BT, int DP>
+// acc[i][c] += sum_k W[ty + ROWS/4 i][k] X[k][4 tx + 64 c ..].
+template <int ROWS, int COLS, int DP>
 __device__ __forceinline__ void accumulate(const float* W, const float* X, int ty, int tx,
-                                           float4 (&acc)[BT / 16][DP / 64]) {
-  constexpr int R = BT / 16, kPitch = DP + 4, kWPitch = BT + 4;
+                                           float4 (&acc)[4][DP / 64]) {
+  constexpr int kPitch = DP + 4, kWPitch = COLS + 4;
 #pragma unroll 2
-  for (int k = 0; k < BT; k += 4) {
-    float4 w[R];
+  for (int k = 0; k < COLS; k += 4) {
+    float4 w[4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      w[i] = *reinterpret_cast<const float4*>(W + (ty + 16 * i) * kWPitch + k);
+    for (int i = 0; i < 4; ++i)
+      w[i] = *reinterpret_cast<const float4*>(W + (ty + ROWS / 4 * i) * kWPitch + k);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -135,12 +140,12 @@ __device__ __forceinline__ void accumulate(const float* W, const float* X, int t
         const float4 x =
             *reinterpret_cast<const float4*>(X + (k + kk) * kPitch + 4 * tx + 64 * c);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const float s = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-          acc[i][c].x = fmaf(s, x.x, acc[i][c].x);
-          acc[i][c].y = fmaf(s, x.y, acc[i][c].y);
-          acc[i][c].z = fmaf(s, x.z, acc[i][c].z);
-          acc[i][c].w = fmaf(s, x.w, acc[i][c].w);
+          const float2 s2 = make_float2(s, s);
+          const float2 lo = tc::fma2(s2, make_float2(x.x, x.y), make_float2(acc[i][c].x, acc[i][c].y));
+          const float2 hi = tc::fma2(s2, make_float2(x.z, x.w), make_float2(acc[i][c].z, acc[i][c].w));
+          acc[i][c] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
       }
   }
@@ -149,51 +154,51 @@ __device__ __forceinline__ void accumulate(const float* W, const float* X, int t
 // Keys past the length may hold anything: load_tile puts zeros in their
 // place, and their scores are masked by selection.
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int DP, int ROWS, int COLS>
+__global__ void __launch_bounds__(4 * ROWS)
     dense_fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                      T* __restrict__ out, float* __restrict__ lse, DenseProblem pb, bool vec) {
-  constexpr int BT = 64, R = BT / 16;
+  constexpr int J = COLS / 16, kThreads = 4 * ROWS;
   extern __shared__ __align__(16) float smf[];
   float* sQ = smf;
-  float* sK = sQ + BT * (DP + 4);
-  float* sV = sK + BT * (DP + 4);
-  float* sP = sV + BT * (DP + 4);  // [query][key]
+  float* sK = sQ + ROWS * (DP + 4);
+  float* sV = sK + COLS * (DP + 4);
+  float* sP = sV + COLS * (DP + 4);  // [query][key]
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int tiles = (pb.Nq + BT - 1) / BT, bh = blockIdx.x / tiles;
-  const int q0 = (int)(blockIdx.x % tiles) * BT, h = bh % pb.H, b = bh / pb.H;
+  const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
+  const int q0 = (int)(blockIdx.x % tiles) * ROWS, h = bh % pb.H, b = bh / pb.H;
   const int hk = h / (pb.H / pb.Hkv);
   const int len = dense_len(pb, b);
   const T* qb = q + b * pb.q.b + h * pb.q.h;
   const T* kb = k + b * pb.k.b + hk * pb.k.h;
   const T* vb = v + b * pb.v.b + hk * pb.v.h;
-  load_tile<T, BT, DP>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
-  int vis[R];
-  float m[R], z[R];
-  float4 o[R][DP / 64];
+  load_tile<T, ROWS, DP, kThreads>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
+  int vis[4];
+  float m[4], z[4];
+  float4 o[4][DP / 64];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int row = q0 + ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int row = q0 + ty + ROWS / 4 * i;
     vis[i] = row < pb.Nq ? dense_visible(pb, len, row) : 0;
     m[i] = -INFINITY;
     z[i] = 0.f;
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int end = dense_visible(pb, len, min(q0 + BT, pb.Nq) - 1);  // keys of the last row
+  const int end = dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1);  // keys of the last row
   const float sl = pb.scale * kLog2e;
-  for (int k0 = 0; k0 < end; k0 += BT) {
+  for (int k0 = 0; k0 < end; k0 += COLS) {
     __syncthreads();
-    load_tile<T, BT, DP>(sK, kb, pb.k.n, k0, len, pb.d, vec);
-    load_tile<T, BT, DP>(sV, vb, pb.v.n, k0, len, pb.d, vec);
+    load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
+    load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
     __syncthreads();
-    float s[R][R];
-    scores<BT, DP>(sQ, sK, ty, tx, s);
+    float s[4][J];
+    scores<ROWS, COLS, DP>(sQ, sK, ty, tx, s);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < 4; ++i) {
       float mt = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
+      for (int j = 0; j < J; ++j) {
         s[i][j] = k0 + tx + 16 * j < vis[i] ? s[i][j] * sl : -INFINITY;
         mt = fmaxf(mt, s[i][j]);
       }
@@ -204,10 +209,10 @@ __global__ void __launch_bounds__(kThreads)
       const float corr = exp2f(m[i] - base);
       float zt = 0.f;
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
+      for (int j = 0; j < J; ++j) {
         const float p = exp2f(s[i][j] - base);
         zt += p;
-        sP[(ty + 16 * i) * (BT + 4) + tx + 16 * j] = p;
+        sP[(ty + ROWS / 4 * i) * (COLS + 4) + tx + 16 * j] = p;
       }
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) zt += __shfl_xor_sync(0xffffffffu, zt, x);
@@ -222,11 +227,11 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncthreads();
-    accumulate<BT, DP>(sP, sV, ty, tx, o);
+    accumulate<ROWS, COLS, DP>(sP, sV, ty, tx, o);
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int row = q0 + ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int row = q0 + ty + ROWS / 4 * i;
     if (row >= pb.Nq) continue;
     const float inv = vis[i] > 0 ? 1.f / z[i] : 0.f;
     T* ob = out + b * pb.out.b + h * pb.out.h + (long)row * pb.out.n;
@@ -243,10 +248,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kDeltaThreads)
     dense_delta_kernel(const T* __restrict__ out, const T* __restrict__ dout,
                        float* __restrict__ delta, DenseProblem pb) {
-  const long row = (long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const long row = (long)blockIdx.x * (kDeltaThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= (long)pb.B * pb.H * pb.Nq) return;
   const int i = (int)(row % pb.Nq);
@@ -263,72 +268,72 @@ __global__ void __launch_bounds__(kThreads)
 // dK and dV of a tile of keys: every query head of the group and every query
 // tile that sees the keys, in order.
 //   P = exp(S - lse), dV = P^T dO, dS = P (dO V^T - delta), dK = scale dS^T Q
-template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int DP, int ROWS, int COLS>
+__global__ void __launch_bounds__(4 * ROWS)
     dense_dkv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                      const float* __restrict__ lse, const float* __restrict__ delta,
                      const T* __restrict__ dout, T* __restrict__ dk, T* __restrict__ dv,
                      DenseProblem pb, bool vec) {
-  constexpr int R = BT / 16;
+  constexpr int J = COLS / 16, kThreads = 4 * ROWS;
   extern __shared__ __align__(16) float smf[];
   float* sK = smf;
-  float* sV = sK + BT * (DP + 4);
-  float* sQ = sV + BT * (DP + 4);
-  float* sG = sQ + BT * (DP + 4);
-  float* sP = sG + BT * (DP + 4);  // [key][query]
-  float* sS = sP + BT * (BT + 4);
+  float* sV = sK + ROWS * (DP + 4);
+  float* sQ = sV + ROWS * (DP + 4);
+  float* sG = sQ + COLS * (DP + 4);
+  float* sP = sG + COLS * (DP + 4);  // [key][query]
+  float* sS = sP + ROWS * (COLS + 4);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int tiles = (pb.Nk + BT - 1) / BT, bh = blockIdx.x / tiles;
-  const int k0 = (int)(blockIdx.x % tiles) * BT, hk = bh % pb.Hkv, b = bh / pb.Hkv;
+  const int tiles = (pb.Nk + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
+  const int k0 = (int)(blockIdx.x % tiles) * ROWS, hk = bh % pb.Hkv, b = bh / pb.Hkv;
   const int len = dense_len(pb, b), group = pb.H / pb.Hkv;
-  load_tile<T, BT, DP>(sK, k + b * pb.k.b + hk * pb.k.h, pb.k.n, k0, len, pb.d, vec);
-  load_tile<T, BT, DP>(sV, v + b * pb.v.b + hk * pb.v.h, pb.v.n, k0, len, pb.d, vec);
-  float4 ak[R][DP / 64], av[R][DP / 64];
+  load_tile<T, ROWS, DP, kThreads>(sK, k + b * pb.k.b + hk * pb.k.h, pb.k.n, k0, len, pb.d, vec);
+  load_tile<T, ROWS, DP, kThreads>(sV, v + b * pb.v.b + hk * pb.v.h, pb.v.n, k0, len, pb.d, vec);
+  float4 ak[4][DP / 64], av[4][DP / 64];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) ak[i][c] = av[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   // the first query that sees key k0
-  const int qfirst = pb.causal ? max(0, k0 - (pb.Nk - pb.Nq)) / BT * BT : 0;
+  const int qfirst = pb.causal ? max(0, k0 - (pb.Nk - pb.Nq)) / COLS * COLS : 0;
   const float sl = pb.scale * kLog2e;
   if (k0 < len) {
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
       const T* qb = q + b * pb.q.b + h * pb.q.h;
       const T* gb = dout + b * pb.dout.b + h * pb.dout.h;
       const long row0 = ((long)b * pb.H + h) * pb.Nq;
-      for (int q0 = qfirst; q0 < pb.Nq; q0 += BT) {
+      for (int q0 = qfirst; q0 < pb.Nq; q0 += COLS) {
         __syncthreads();
-        load_tile<T, BT, DP>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
-        load_tile<T, BT, DP>(sG, gb, pb.dout.n, q0, pb.Nq, pb.d, vec);
+        load_tile<T, COLS, DP, kThreads>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
+        load_tile<T, COLS, DP, kThreads>(sG, gb, pb.dout.n, q0, pb.Nq, pb.d, vec);
         __syncthreads();
-        float s[R][R], dp[R][R];
-        scores<BT, DP>(sQ, sK, ty, tx, s);
-        scores<BT, DP>(sG, sV, ty, tx, dp);
+        float s[4][J], dp[4][J];
+        scores<ROWS, COLS, DP>(sK, sQ, ty, tx, s);
+        scores<ROWS, COLS, DP>(sV, sG, ty, tx, dp);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const int row = q0 + ty + 16 * i;
+        for (int j = 0; j < J; ++j) {
+          const int row = q0 + tx + 16 * j;
           const bool ok = row < pb.Nq;
           const int vis = ok ? dense_visible(pb, len, row) : 0;
           const float l2 = ok ? __ldg(lse + row0 + row) * kLog2e : 0.f;
           const float dl = ok ? __ldg(delta + row0 + row) : 0.f;
 #pragma unroll
-          for (int j = 0; j < R; ++j) {
-            const bool see = k0 + tx + 16 * j < vis;
+          for (int i = 0; i < 4; ++i) {
+            const int key = ty + ROWS / 4 * i, at = key * (COLS + 4) + tx + 16 * j;
+            const bool see = k0 + key < vis;
             const float p = see ? exp2f(fmaf(s[i][j], sl, -l2)) : 0.f;
-            const int at = (tx + 16 * j) * (BT + 4) + ty + 16 * i;
             sP[at] = p;
             sS[at] = see ? p * (dp[i][j] - dl) : 0.f;
           }
         }
         __syncthreads();
-        accumulate<BT, DP>(sP, sG, ty, tx, av);
-        accumulate<BT, DP>(sS, sQ, ty, tx, ak);
+        accumulate<ROWS, COLS, DP>(sP, sG, ty, tx, av);
+        accumulate<ROWS, COLS, DP>(sS, sQ, ty, tx, ak);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int row = k0 + ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int row = k0 + ty + ROWS / 4 * i;
     if (row >= pb.Nk) continue;
     T* kr = dk + b * pb.dk.b + hk * pb.dk.h + (long)row * pb.dk.n;
     T* vr = dv + b * pb.dv.b + hk * pb.dv.h + (long)row * pb.dv.n;
@@ -343,33 +348,33 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // dQ of a tile of queries: dQ = scale dS K over the tiles of visible keys.
-template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int DP, int ROWS, int COLS>
+__global__ void __launch_bounds__(4 * ROWS)
     dense_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                     const float* __restrict__ lse, const float* __restrict__ delta,
                     const T* __restrict__ dout, T* __restrict__ dq, DenseProblem pb, bool vec) {
-  constexpr int R = BT / 16;
+  constexpr int J = COLS / 16, kThreads = 4 * ROWS;
   extern __shared__ __align__(16) float smf[];
   float* sQ = smf;
-  float* sG = sQ + BT * (DP + 4);
-  float* sK = sG + BT * (DP + 4);
-  float* sV = sK + BT * (DP + 4);
-  float* sS = sV + BT * (DP + 4);  // [query][key]
+  float* sG = sQ + ROWS * (DP + 4);
+  float* sK = sG + ROWS * (DP + 4);
+  float* sV = sK + COLS * (DP + 4);
+  float* sS = sV + COLS * (DP + 4);  // [query][key]
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int tiles = (pb.Nq + BT - 1) / BT, bh = blockIdx.x / tiles;
-  const int q0 = (int)(blockIdx.x % tiles) * BT, h = bh % pb.H, b = bh / pb.H;
+  const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
+  const int q0 = (int)(blockIdx.x % tiles) * ROWS, h = bh % pb.H, b = bh / pb.H;
   const int hk = h / (pb.H / pb.Hkv);
   const int len = dense_len(pb, b);
   const T* kb = k + b * pb.k.b + hk * pb.k.h;
   const T* vb = v + b * pb.v.b + hk * pb.v.h;
-  load_tile<T, BT, DP>(sQ, q + b * pb.q.b + h * pb.q.h, pb.q.n, q0, pb.Nq, pb.d, vec);
-  load_tile<T, BT, DP>(sG, dout + b * pb.dout.b + h * pb.dout.h, pb.dout.n, q0, pb.Nq, pb.d, vec);
-  int vis[R];
-  float l2[R], dl[R];
-  float4 acc[R][DP / 64];
+  load_tile<T, ROWS, DP, kThreads>(sQ, q + b * pb.q.b + h * pb.q.h, pb.q.n, q0, pb.Nq, pb.d, vec);
+  load_tile<T, ROWS, DP, kThreads>(sG, dout + b * pb.dout.b + h * pb.dout.h, pb.dout.n, q0, pb.Nq, pb.d, vec);
+  int vis[4];
+  float l2[4], dl[4];
+  float4 acc[4][DP / 64];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int row = q0 + ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int row = q0 + ty + ROWS / 4 * i;
     const bool ok = row < pb.Nq;
     const long at = ((long)b * pb.H + h) * pb.Nq + row;
     vis[i] = ok ? dense_visible(pb, len, row) : 0;
@@ -378,30 +383,30 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int end = dense_visible(pb, len, min(q0 + BT, pb.Nq) - 1);
+  const int end = dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1);
   const float sl = pb.scale * kLog2e;
-  for (int k0 = 0; k0 < end; k0 += BT) {
+  for (int k0 = 0; k0 < end; k0 += COLS) {
     __syncthreads();
-    load_tile<T, BT, DP>(sK, kb, pb.k.n, k0, len, pb.d, vec);
-    load_tile<T, BT, DP>(sV, vb, pb.v.n, k0, len, pb.d, vec);
+    load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
+    load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
     __syncthreads();
-    float s[R][R], dp[R][R];
-    scores<BT, DP>(sQ, sK, ty, tx, s);
-    scores<BT, DP>(sG, sV, ty, tx, dp);
+    float s[4][J], dp[4][J];
+    scores<ROWS, COLS, DP>(sQ, sK, ty, tx, s);
+    scores<ROWS, COLS, DP>(sG, sV, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
+      for (int j = 0; j < J; ++j) {
         const bool see = k0 + tx + 16 * j < vis[i];
         const float p = exp2f(fmaf(s[i][j], sl, -l2[i]));
-        sS[(ty + 16 * i) * (BT + 4) + tx + 16 * j] = see ? p * (dp[i][j] - dl[i]) : 0.f;
+        sS[(ty + ROWS / 4 * i) * (COLS + 4) + tx + 16 * j] = see ? p * (dp[i][j] - dl[i]) : 0.f;
       }
     __syncthreads();
-    accumulate<BT, DP>(sS, sK, ty, tx, acc);
+    accumulate<ROWS, COLS, DP>(sS, sK, ty, tx, acc);
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int row = q0 + ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int row = q0 + ty + ROWS / 4 * i;
     if (row >= pb.Nq) continue;
     T* qr = dq + b * pb.dq.b + h * pb.dq.h + (long)row * pb.dq.n;
 #pragma unroll
@@ -418,42 +423,79 @@ bool rows_allow_four(const void* p, const HeadStrides& s, size_t elt) {
          s.n % 4 == 0;
 }
 
-template <typename T, int DP>
-cudaError_t forward_dp(const T* q, const T* k, const T* v, T* out, float* lse,
-                       const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
-  const size_t smem = (3 * 64 * (DP + 4) + 64 * 68) * sizeof(float);
-  cudaError_t e = allow_smem<dense_fwd_kernel<T, DP>>((int)smem);
+// Rows of a CTA: 64 read each streamed tile half as often, 32 where 64 would
+// leave the SMs fewer than four CTAs each.
+inline bool few(long rows, long heads) { return (rows + 63) / 64 * heads < 4L * num_sms(); }
+
+template <typename T, int DP, int ROWS, int COLS>
+cudaError_t forward_rows(const T* q, const T* k, const T* v, T* out, float* lse,
+                         const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
+  constexpr int smem =
+      ((ROWS + 2 * COLS) * (DP + 4) + ROWS * (COLS + 4)) * (int)sizeof(float);
+  constexpr auto kernel = dense_fwd_kernel<T, DP, ROWS, COLS>;
+  cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)((pb.Nq + 63) / 64) * pb.H * pb.B;
+  const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B;
   return timed_launch("dense_fwd_simt", stream, launches, [&] {
-    dense_fwd_kernel<T, DP><<<grid, kThreads, smem, stream>>>(q, k, v, out, lse, pb, vec);
+    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, out, lse, pb, vec);
   });
 }
 
-template <typename T, int DP, int BT>
+template <typename T, int DP, int COLS>
+cudaError_t forward_dp(const T* q, const T* k, const T* v, T* out, float* lse,
+                       const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
+  return few(pb.Nq, (long)pb.H * pb.B)
+             ? forward_rows<T, DP, 32, COLS>(q, k, v, out, lse, pb, vec, stream, launches)
+             : forward_rows<T, DP, 64, COLS>(q, k, v, out, lse, pb, vec, stream, launches);
+}
+
+template <typename T, int DP, int ROWS, int COLS>
+cudaError_t dkv_rows(const T* q, const T* k, const T* v, const float* lse, const float* delta,
+                     const T* dout, T* dk, T* dv, const DenseProblem& pb, bool vec,
+                     cudaStream_t stream, int* launches) {
+  constexpr int smem =
+      (2 * (ROWS + COLS) * (DP + 4) + 2 * ROWS * (COLS + 4)) * (int)sizeof(float);
+  constexpr auto kernel = dense_dkv_kernel<T, DP, ROWS, COLS>;
+  cudaError_t e = allow_smem<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)((pb.Nk + ROWS - 1) / ROWS) * pb.Hkv * pb.B;
+  return timed_launch("dense_dkv_simt", stream, launches, [&] {
+    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, lse, delta, dout, dk, dv, pb, vec);
+  });
+}
+
+template <typename T, int DP, int ROWS, int COLS>
+cudaError_t dq_rows(const T* q, const T* k, const T* v, const float* lse, const float* delta,
+                    const T* dout, T* dq, const DenseProblem& pb, bool vec, cudaStream_t stream,
+                    int* launches) {
+  constexpr int smem =
+      (2 * (ROWS + COLS) * (DP + 4) + ROWS * (COLS + 4)) * (int)sizeof(float);
+  constexpr auto kernel = dense_dq_kernel<T, DP, ROWS, COLS>;
+  cudaError_t e = allow_smem<kernel>(smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B;
+  return timed_launch("dense_dq_simt", stream, launches, [&] {
+    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, lse, delta, dout, dq, pb, vec);
+  });
+}
+
+// TALL: rows of a CTA where there are many.
+template <typename T, int DP, int TALL, int COLS>
 cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, const float* delta,
                         const T* dout, T* dq, T* dk, T* dv, const DenseProblem& pb, bool vec,
                         cudaStream_t stream, int* launches) {
-  const size_t kv = (4 * BT * (DP + 4) + 2 * BT * (BT + 4)) * sizeof(float);
-  const size_t qs = (4 * BT * (DP + 4) + BT * (BT + 4)) * sizeof(float);
   cudaError_t e = cudaSuccess;
-  if (pb.Nk > 0) {
-    if ((e = allow_smem<dense_dkv_kernel<T, DP, BT>>((int)kv)) != cudaSuccess) return e;
-    e = timed_launch("dense_dkv_simt", stream, launches, [&] {
-      dense_dkv_kernel<T, DP, BT>
-          <<<(unsigned)((pb.Nk + BT - 1) / BT) * pb.Hkv * pb.B, kThreads, kv, stream>>>(
-              q, k, v, lse, delta, dout, dk, dv, pb, vec);
-    });
-    if (e != cudaSuccess) return e;
-  }
-  if (pb.Nq > 0) {
-    if ((e = allow_smem<dense_dq_kernel<T, DP, BT>>((int)qs)) != cudaSuccess) return e;
-    e = timed_launch("dense_dq_simt", stream, launches, [&] {
-      dense_dq_kernel<T, DP, BT>
-          <<<(unsigned)((pb.Nq + BT - 1) / BT) * pb.H * pb.B, kThreads, qs, stream>>>(
-              q, k, v, lse, delta, dout, dq, pb, vec);
-    });
-  }
+  if (pb.Nk > 0)
+    e = few(pb.Nk, (long)pb.Hkv * pb.B)
+            ? dkv_rows<T, DP, 32, COLS>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
+                                        launches)
+            : dkv_rows<T, DP, TALL, COLS>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
+                                          launches);
+  if (e == cudaSuccess && pb.Nq > 0)
+    e = few(pb.Nq, (long)pb.H * pb.B)
+            ? dq_rows<T, DP, 32, COLS>(q, k, v, lse, delta, dout, dq, pb, vec, stream, launches)
+            : dq_rows<T, DP, TALL, COLS>(q, k, v, lse, delta, dout, dq, pb, vec, stream,
+                                         launches);
   return e;
 }
 
@@ -466,9 +508,9 @@ cudaError_t dense_simt_forward(const T* q, const T* k, const T* v, T* out, float
   const bool vec = pb.d % 4 == 0 && rows_allow_four(q, pb.q, sizeof(T)) &&
                    rows_allow_four(k, pb.k, sizeof(T)) && rows_allow_four(v, pb.v, sizeof(T)) &&
                    rows_allow_four(out, pb.out, sizeof(T));
-  if (pb.d <= 64) return forward_dp<T, 64>(q, k, v, out, lse, pb, vec, stream, launches);
-  if (pb.d <= 128) return forward_dp<T, 128>(q, k, v, out, lse, pb, vec, stream, launches);
-  return forward_dp<T, 256>(q, k, v, out, lse, pb, vec, stream, launches);
+  if (pb.d <= 64) return forward_dp<T, 64, 64>(q, k, v, out, lse, pb, vec, stream, launches);
+  if (pb.d <= 128) return forward_dp<T, 128, 64>(q, k, v, out, lse, pb, vec, stream, launches);
+  return forward_dp<T, 256, 32>(q, k, v, out, lse, pb, vec, stream, launches);
 }
 
 template <typename T>
@@ -476,9 +518,9 @@ cudaError_t dense_delta(const T* out, const T* dout, float* delta, const DensePr
                         cudaStream_t stream, int* launches) {
   const long rows = (long)pb.B * pb.H * pb.Nq;
   if (rows == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned blocks = (unsigned)((rows + kDeltaThreads / 32 - 1) / (kDeltaThreads / 32));
   return timed_launch("dense_delta", stream, launches, [&] {
-    dense_delta_kernel<T><<<blocks, kThreads, 0, stream>>>(out, dout, delta, pb);
+    dense_delta_kernel<T><<<blocks, kDeltaThreads, 0, stream>>>(out, dout, delta, pb);
   });
 }
 
@@ -494,13 +536,13 @@ cudaError_t dense_simt_backward(const T* q, const T* k, const T* v, const T* out
   cudaError_t e = dense_delta<T>(out, dout, delta, pb, stream, launches);
   if (e != cudaSuccess) return e;
   if (pb.d <= 64)
-    return backward_dp<T, 64, 64>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
+    return backward_dp<T, 64, 64, 64>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
                                   launches);
   if (pb.d <= 128)
-    return backward_dp<T, 128, 64>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
+    return backward_dp<T, 128, 64, 64>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
                                    launches);
-  // 32-row tiles: four 64-row tiles of 256 channels exceed shared memory
-  return backward_dp<T, 256, 32>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
+  // four 64-row tiles of 256 channels exceed shared memory
+  return backward_dp<T, 256, 32, 32>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
                                  launches);
 }
 
