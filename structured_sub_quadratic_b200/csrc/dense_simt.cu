@@ -56,12 +56,22 @@ __device__ __forceinline__ void store4<bf16>(bf16* p, float4 v) {
 template <typename T, int BT, int DP, int THREADS>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, long stride, int r0, int n,
                                           int d, bool vec) {
-  constexpr int kPitch = DP + 4;
-  for (int x = threadIdx.x; x < BT * (DP / 4); x += THREADS) {
-    const int r = x / (DP / 4), c = x % (DP / 4) * 4;
+  constexpr int kPitch = DP + 4, kEach = BT * (DP / 4) / THREADS;
+  static_assert(BT * (DP / 4) % THREADS == 0, "whole loads per thread");
+#pragma unroll 8
+  for (int i = 0; i < kEach; ++i) {
+    const int x = i * THREADS + (int)threadIdx.x, r = x / (DP / 4), c = x % (DP / 4) * 4;
+    float* to = dst + r * kPitch + c;
+    const bool there = r0 + r < n && c < d;
+    const T* p = src + (there ? (long)(r0 + r) * stride + c : 0);
+    if (sizeof(T) == 4 && vec) {  // straight to shared memory, all of a tile in flight
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)),
+                   "l"(p), "r"(there ? 16 : 0)
+                   : "memory");
+      continue;
+    }
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < n && c < d) {
-      const T* p = src + (long)(r0 + r) * stride + c;
+    if (there) {
       if (vec) {
         v = load4(p);
       } else {
@@ -71,8 +81,15 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, long stride,
         if (c + 3 < d) v.w = to_f32(p[3]);
       }
     }
-    *reinterpret_cast<float4*>(dst + r * kPitch + c) = v;
+    *reinterpret_cast<float4*>(to) = v;
   }
+}
+
+// Every tile that this thread's load_tile calls asked for is there, for all
+// threads of the CTA.
+__device__ __forceinline__ void tiles_arrived() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
 }
 
 template <typename T>
@@ -191,7 +208,7 @@ __global__ void __launch_bounds__(4 * ROWS)
     __syncthreads();
     load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
     load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
-    __syncthreads();
+    tiles_arrived();
     float s[4][J];
     scores<ROWS, COLS, DP>(sQ, sK, ty, tx, s);
 #pragma unroll
@@ -229,6 +246,7 @@ __global__ void __launch_bounds__(4 * ROWS)
     __syncthreads();
     accumulate<ROWS, COLS, DP>(sP, sV, ty, tx, o);
   }
+  tiles_arrived();  // (a CTA without keys still has its queries in flight)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = q0 + ty + ROWS / 4 * i;
@@ -305,7 +323,7 @@ __global__ void __launch_bounds__(4 * ROWS)
         __syncthreads();
         load_tile<T, COLS, DP, kThreads>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
         load_tile<T, COLS, DP, kThreads>(sG, gb, pb.dout.n, q0, pb.Nq, pb.d, vec);
-        __syncthreads();
+        tiles_arrived();
         float s[4][J], dp[4][J];
         scores<ROWS, COLS, DP>(sK, sQ, ty, tx, s);
         scores<ROWS, COLS, DP>(sV, sG, ty, tx, dp);
@@ -331,6 +349,7 @@ __global__ void __launch_bounds__(4 * ROWS)
       }
     }
   }
+  tiles_arrived();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = k0 + ty + ROWS / 4 * i;
@@ -389,7 +408,7 @@ __global__ void __launch_bounds__(4 * ROWS)
     __syncthreads();
     load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
     load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
-    __syncthreads();
+    tiles_arrived();
     float s[4][J], dp[4][J];
     scores<ROWS, COLS, DP>(sQ, sK, ty, tx, s);
     scores<ROWS, COLS, DP>(sG, sV, ty, tx, dp);
@@ -404,6 +423,7 @@ __global__ void __launch_bounds__(4 * ROWS)
     __syncthreads();
     accumulate<ROWS, COLS, DP>(sS, sK, ty, tx, acc);
   }
+  tiles_arrived();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = q0 + ty + ROWS / 4 * i;

@@ -570,22 +570,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float* rows = reinterpret_cast<float*>(smem + L::kRowOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* kv_full = bars;
-  uint64_t* q_full = bars + 1;   // [stages]: Q and the row statistics
-  uint64_t* g_full = bars + 3;   // [stages]: dO
-  uint64_t* empty = bars + 5;    // [stages]
-  uint64_t* s_full = bars + 7;
-  uint64_t* dp_full = bars + 8;
-  uint64_t* p_full = bars + 9;
-  uint64_t* ds_full = bars + 10;
-  uint64_t* done = bars + 11;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 13);
+  uint64_t* q_full = bars + 1;   // [stages]
+  uint64_t* q_empty = bars + 3;
+  uint64_t* g_full = bars + 5;   // [stages]: dO
+  uint64_t* g_empty = bars + 7;
+  uint64_t* row_full = bars + 9;  // [stages]: lse and delta (free with Q's slot)
+  uint64_t* s_full = bars + 11;
+  uint64_t* dp_full = bars + 12;
+  uint64_t* p_full = bars + 13;
+  uint64_t* ds_full = bars + 14;
+  uint64_t* done = bars + 15;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 17);
   if (tid == 0) {
     mbar_init(kv_full, 1);
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(q_full + s, 32);
+      mbar_init(q_full + s, 1);
+      mbar_init(q_empty + s, 1);
       mbar_init(g_full + s, 1);
-      mbar_init(empty + s, 1);
+      mbar_init(g_empty + s, 1);
+      mbar_init(row_full + s, 1);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
@@ -606,43 +610,59 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   if (warp == 8) {
     // ---- TMA: K and V, then Q and dO tile by tile with lse and delta ----
-    int issued = 0;
+    int qs = 0, gs = 0;  // tiles issued
     if (lane == 0 && n > 0) {
       mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
       load_tile<D>(smem + L::kAOff, mk, kv_full, k0, hk, b);
       load_tile<D>(smem + L::kBOff, mv, kv_full, k0, hk, b);
     }
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int st = i & 1, h = hk * group + i / per, q0 = (first + i % per) * kTile;
-      if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait(empty + st, ((i >> 1) - 1) & 1,
-                                                         abort_flag, a.status));
-      if (!ok) break;
+    int h = hk * group, q0 = first * kTile;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      const uint32_t par = ((i >> 1) - 1) & 1;
+      // the row statistics are under way before the tile's slots are free
       const long at = ((long)b * pb.H + h) * pb.Nq;
-      for (int x = lane; x < kTile; x += 32) {
+      float l2[4], dl[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
         // a row outside the tensor or without keys: exp(S - inf) = 0
-        const int row = q0 + x;
+        const int row = q0 + x * 32 + lane;
         const bool live = row < pb.Nq && dense_visible(pb, len, row) > 0;
-        rows[st * 256 + x] = live ? __ldg(a.lse + at + row) * kLog2e : INFINITY;
-        rows[st * 256 + kTile + x] = live ? __ldg(a.delta + at + row) : 0.f;
+        l2[x] = live ? __ldg(a.lse + at + row) * kLog2e : INFINITY;
+        dl[x] = live ? __ldg(a.delta + at + row) : 0.f;
       }
+      if (i >= 2 && !warp_wait(g_empty + st, par, abort_flag, a.status)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(g_full + st, L::kTileBytes);
+        load_tile<D>(smem + L::kYOff + st * L::kTileBytes, mg, g_full + st, q0, h, b);
+      }
+      gs = i + 1;
+      if (i >= 2 && !warp_wait(q_empty + st, par, abort_flag, a.status)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(q_full + st, L::kTileBytes);
         load_tile<D>(smem + L::kXOff + st * L::kTileBytes, mq, q_full + st, q0, h, b);
-        mbar_arrive_expect_tx(g_full + st, L::kTileBytes);
-        load_tile<D>(smem + L::kYOff + st * L::kTileBytes, mg, g_full + st, q0, h, b);
-      } else {
-        mbar_arrive(q_full + st);
       }
-      issued = i + 1;
+      qs = i + 1;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        rows[st * 256 + x * 32 + lane] = l2[x];
+        rows[st * 256 + kTile + x * 32 + lane] = dl[x];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(row_full + st);
+      q0 += kTile;
+      if (q0 >= pb.Nq) {
+        q0 = first * kTile;
+        ++h;
+      }
     }
     if (lane == 0 && n > 0 && *abort_flag) {  // wait (bounded) for the loads in flight
       drain_bar(kv_full, 0);
-      for (int s = 0; s < L::kStages; ++s)
-        if (issued > s) {
-          drain_bar(q_full + s, ((issued - 1 - s) >> 1) & 1);
-          drain_bar(g_full + s, ((issued - 1 - s) >> 1) & 1);
-        }
+      for (int s = 0; s < L::kStages; ++s) {
+        if (qs > s) drain_bar(q_full + s, ((qs - 1 - s) >> 1) & 1);
+        if (gs > s) drain_bar(g_full + s, ((gs - 1 - s) >> 1) & 1);
+      }
     }
   } else if (warp == 9) {
     // ---- MMA issue ----
@@ -674,6 +694,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!(ok = warp_wait(p_full, i & 1, abort_flag, a.status))) break;
         tc_fence_after();
         mma_halves<D>(tmem + L::kAccCol, tmem, ym + st * kStep, i > 0);
+        warp_commit(g_empty + st);
         if (more) {  // (in order: over P once dV has read it)
           mma_nt<D>(tmem, dk, xk + s1 * kStep);
           warp_commit(s_full);
@@ -682,7 +703,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!(ok = warp_wait(ds_full, i & 1, abort_flag, a.status))) break;
         tc_fence_after();
         mma_halves<D>(tmem + L::kAccCol + D, tmem + L::kDPCol, xm + st * kStep, i > 0);
-        warp_commit(empty + st);
+        warp_commit(q_empty + st);
         if (more) {
           mma_nt<D>(tmem + L::kDPCol, dv, yk + s1 * kStep);
           warp_commit(dp_full);
@@ -699,11 +720,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float sl = pb.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
     bool ok = true;
+    int q0 = first * kTile;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int st = i & 1, q0 = (first + i % per) * kTile;
+      const int st = i & 1;
       const float* lse2 = rows + st * 256 + half * 64;
       const float* delta = lse2 + kTile;
-      if (!(ok = mbar_wait(q_full + st, (i >> 1) & 1, abort_flag, a.status))) break;
+      if (!(ok = mbar_wait(row_full + st, (i >> 1) & 1, abort_flag, a.status))) break;
       if (!(ok = mbar_wait(s_full, i & 1, abort_flag, a.status))) break;
       tc_fence_after();
       float p[64];
@@ -749,6 +772,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       store_half(tp, d);
       tmem_wait_st();
       warp_arrive(ds_full);
+      q0 = q0 + kTile < pb.Nq ? q0 + kTile : first * kTile;
     }
     if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
     tc_fence_after();
