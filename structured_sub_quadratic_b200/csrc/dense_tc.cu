@@ -168,29 +168,29 @@ template <int D>
 struct FwdLayout {
   static constexpr int kCh = D / 64, kStages = D == 128 ? 2 : 3;
   static constexpr int kTileBytes = kCh * kChunk;
+  static constexpr int kTiles = D == 128 ? 2 : 1;  // 128-row tiles of a CTA
+  static constexpr int kThreads = kTiles * kTile + 64, kTmaWarp = kTiles * 4;
   static constexpr int kQOff = 0;
-  static constexpr int kKOff = kQOff + 2 * kTileBytes;
+  static constexpr int kKOff = kQOff + kTiles * kTileBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kBarOff = kVOff + kStages * kTileBytes;
   static constexpr int kBytes = kBarOff + 32 * 8;
-  // TMEM columns: S of tile t and buffer y at 128 t + 64 y, O at 256 + D t
-  static constexpr uint32_t kTmemCols = 512, kOCol = 256;
+  // TMEM columns: S of tile t and buffer y at 128 t + 64 y, then O of tile t
+  static constexpr uint32_t kTmemCols = kTiles * 256, kOCol = kTiles * kTile;
   // of 16 pairs of exponentials, those on the FMA pipe
-  static constexpr int kFmaPairs = 4;
-  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static constexpr int kFmaPairs = D == 64 ? 4 : 0;
+  static_assert(kBytes * (3 - kTiles) <= 226 * 1024, "shared memory");
 };
 
 struct FwdArgs {
   float* lse;
   DenseProblem pb;
-  int tiles;  // 256-row tiles of a head
+  int tiles;  // CTAs of a head
   int* status;
 };
 
-constexpr int kFwdThreads = 320;
-
 template <int D>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTiles)
     dense_fwd_tc_kernel(const __grid_constant__ TileMap mq, const __grid_constant__ TileMap mk,
                         const __grid_constant__ TileMap mv, const __grid_constant__ TileMap mo,
                         const __grid_constant__ FwdArgs a) {
@@ -212,12 +212,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bh = blockIdx.x / a.tiles;
   }
   const int h = bh % pb.H, b = bh / pb.H, hk = h / (pb.H / pb.Hkv);
-  const int q0 = tile * 2 * kTile;
+  const int q0 = tile * L::kTiles * kTile;
   const int len = dense_len(pb, b);
   // steps of the two row tiles, key tiles, and the last one's rows past the length
-  int nt[2];
+  int nt[2] = {0, 0};
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < L::kTiles; ++t) {
     const int r0 = q0 + t * kTile;
     nt[t] = r0 < pb.Nq
                 ? (dense_visible(pb, len, min(r0 + kTile, pb.Nq) - 1) + kStep - 1) / kStep
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == L::kTmaWarp + 1) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp == 8) {
+  if (warp == L::kTmaWarp) {
     // ---- TMA: Q, then K and V tile by tile ----
     bool ok = true;
     int kt = 0, vt = 0;  // tiles issued
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tma_prefetch_desc(&mq.map);
       tma_prefetch_desc(&mk.map);
       tma_prefetch_desc(&mv.map);
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < L::kTiles; ++t)
         if (q0 + t * kTile < pb.Nq) {
           mbar_arrive_expect_tx(q_full + t, L::kTileBytes);
           load_tile<D>(smem + L::kQOff + t * L::kTileBytes, mq, q_full + t, q0 + t * kTile, h, b);
@@ -307,14 +307,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
     }
     if (lane == 0 && *abort_flag) {  // wait (bounded) for the loads in flight
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < L::kTiles; ++t)
         if (q0 + t * kTile < pb.Nq) drain_bar(q_full + t, 0);
       for (int s = 0; s < L::kStages; ++s) {
         if (kt > s) drain_bar(k_full + s, ((kt - 1 - s) / L::kStages) & 1);
         if (vt > s) drain_bar(v_full + s, ((vt - 1 - s) / L::kStages) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == L::kTmaWarp + 1) {
     // ---- MMA issue ----
     if (n > 0) {
       const uint64_t dq = desc_kmajor(smem_u32(smem + L::kQOff));
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       };
       bool ok = warp_wait(k_full, 0, abort_flag, a.status);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < L::kTiles; ++t)
         if (ok && nt[t] > 0 && (ok = warp_wait(q_full + t, 0, abort_flag, a.status))) {
 #pragma unroll
           for (int y = 0; y < 2; ++y)
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < L::kTiles; ++t) {
             const int u = 2 * j + y;
             if (!ok || u >= nt[t] || !(ok = warp_wait(p_full + 2 * t + y, j & 1, abort_flag, a.status)))
               continue;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == L::kTmaWarp + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
@@ -1064,13 +1064,14 @@ bool make_tile_map(TileMap* m, const void* base, const HeadStrides& s, int B, in
 
 template <int D>
 cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mo,
-                      const FwdArgs& a, cudaStream_t stream, int* launches) {
+                      FwdArgs a, cudaStream_t stream, int* launches) {
   using L = FwdLayout<D>;
+  a.tiles = (a.pb.Nq + L::kTiles * kTile - 1) / (L::kTiles * kTile);
   const cudaError_t e = allow_smem<dense_fwd_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)a.tiles * a.pb.H * a.pb.B;
   return timed_launch("dense_fwd_tc", stream, launches, [&] {
-    dense_fwd_tc_kernel<D><<<grid, kFwdThreads, L::kBytes, stream>>>(mq, mk, mv, mo, a);
+    dense_fwd_tc_kernel<D><<<grid, L::kThreads, L::kBytes, stream>>>(mq, mk, mv, mo, a);
   });
 }
 
@@ -1113,7 +1114,7 @@ cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* 
       !make_tile_map(&mv, v, pb.v, pb.B, pb.Hkv, pb.Nk, pb.d) ||
       !make_tile_map(&mo, out, pb.out, pb.B, pb.H, pb.Nq, pb.d))
     return cudaErrorInvalidValue;
-  const FwdArgs a = {lse, pb, (pb.Nq + 2 * kTile - 1) / (2 * kTile), status};
+  FwdArgs a = {lse, pb, 0, status};
   return pb.d <= 64 ? forward_d<64>(mq, mk, mv, mo, a, stream, launches)
                     : forward_d<128>(mq, mk, mv, mo, a, stream, launches);
 }
