@@ -265,11 +265,17 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
  * A row without a visible key gets out = 0 and lse = -inf.  Keys past the
  * length may hold anything (NaN included); keys hidden by `causal` alone must
  * be finite.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
- * for the product with v, sums are fp32.  scale > 0. */
+ * for the product with v, sums are fp32.  scale > 0.  Few queries over many
+ * keys are split over the keys and joined in order; workspace: device,
+ * 16-byte aligned, monarch_attn_dense_fwd_workspace_bytes (0 where nothing is
+ * split). */
 MONARCH_API int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* v,
                                        void* out, float* lse, int B, int H, int Hkv, int Nq,
                                        int Nk, int d, const long long* strides, int causal,
-                                       const int* k_lens, float scale, cudaStream_t stream);
+                                       const int* k_lens, float scale, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+MONARCH_API size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int H, int Nq, int Nk,
+                                                          int d);
 
 /* Gradients of sum(out * dout) with respect to q, k and v; the probabilities
  * are recomputed from q, k and lse.  out and lse: what

@@ -43,7 +43,9 @@ SIGNATURES = {
     "monarch_attn_fwd_padded": (_I, [_I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                      _I, _P]),
     "monarch_attn_bwd": (_I, [_I, _P, _P, _P, _P, _P, _P, _P, *_SIZES, _P]),
-    "monarch_attn_dense_fwd": (_I, [_I, _P, _P, _P, _P, _P, *[_I] * 6, _P, _I, _P, _F, _P]),
+    "monarch_attn_dense_fwd": (_I, [_I, _P, _P, _P, _P, _P, *[_I] * 6, _P, _I, _P, _F, _P, _Z,
+                                    _P]),
+    "monarch_attn_dense_fwd_workspace_bytes": (_Z, [_I] * 6),
     "monarch_attn_dense_bwd": (_I, [_I, *[_P] * 9, *[_I] * 6, _P, _I, _P, _F, _P, _Z, _P]),
     "monarch_attn_dense_bwd_workspace_bytes": (_Z, [_I, _I, _I]),
     "monarch_attn_dense_decode": (_I, [_I, *[_P] * 7, *[_I] * 7, _P, _F, _P, _Z, _P]),
@@ -317,6 +319,12 @@ def _strides(*tensors):
     return _STRIDES[len(tensors)](*flat)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_need(call, device_index, *sizes):
+    """Bytes of workspace of a call (a function of the sizes and the device)."""
+    return getattr(load_library(), f"monarch_attn_{call}_workspace_bytes")(*sizes)
+
+
 def _like(t):
     """Uninitialised, t's shape, and t's strides unless its elements repeat."""
     return t.new_empty(t.shape) if 0 in t.stride() else torch.empty_like(t)
@@ -358,10 +366,12 @@ def monarch_attn_dense_fwd(q, k, v, causal=False, k_lens=None, scale=None, out=N
     if out is None:
         out = _like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    need = _workspace_need("dense_fwd", q.get_device(), dtype, B, H, Nq, Nk, d)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     _check(lib.monarch_attn_dense_fwd(
         dtype, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
         Hkv, Nq, Nk, d, _strides(q, k, v, out), bool(causal), lens, scale,
-        _current(q.get_device())))
+        ws.data_ptr() if need else None, need, _current(q.get_device())))
     return out, lse
 
 
@@ -392,12 +402,6 @@ def monarch_attn_dense_bwd(q, k, v, out, lse, dout, causal=False, k_lens=None, s
         _strides(q, k, v, out, dout, dq, dk, dv), bool(causal), lens, scale, ws.data_ptr(), need,
         _current(q.get_device())))
     return dq, dk, dv
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_workspace(device_index, *sizes):
-    """Bytes that a decode call of these sizes needs (a function of the sizes and the device)."""
-    return load_library().monarch_attn_dense_decode_workspace_bytes(*sizes)
 
 
 def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None, out=None,
@@ -435,14 +439,15 @@ def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None,
     if out is None:
         out = _like(q)
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    need = _decode_workspace(q.get_device(), dtype, B, H, Hkv, d, page_size, max_pages)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    need = _workspace_need("dense_decode", q.get_device(), dtype, B, H, Hkv, d, page_size,
+                           max_pages)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     strides = _STRIDES[4](*q.stride()[:2], 0, *k_cache.stride()[:3], *v_cache.stride()[:3],
                           *out.stride()[:2], 0)
     _check(lib.monarch_attn_dense_decode(
         dtype, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, len_ptr,
         out.data_ptr(), lse.data_ptr(), B, H, Hkv, d, pages, page_size, max_pages, strides,
-        1.0 / math.sqrt(d) if scale is None else scale, ws.data_ptr(), need,
+        1.0 / math.sqrt(d) if scale is None else scale, ws.data_ptr() if need else None, need,
         _current(q.get_device())))
     return out, lse
 

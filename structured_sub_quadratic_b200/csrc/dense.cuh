@@ -54,9 +54,11 @@ cudaError_t dense_simt_backward(const T* q, const T* k, const T* v, const T* out
 // Tensor-core kernels (dense_tc.cu): bf16, d a multiple of 8 up to 128, rows
 // of 16-byte alignment.
 bool dense_tc_rows(const void* p, const HeadStrides& s, int N, int d);
+// Bytes of workspace that the forward pass needs (0: none).
+size_t dense_tc_workspace_bytes(const DenseProblem& pb);
 cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
-                             const DenseProblem& pb, int* status, cudaStream_t stream,
-                             int* launches);
+                             const DenseProblem& pb, float* workspace, int* status,
+                             cudaStream_t stream, int* launches);
 cudaError_t dense_tc_backward(const bf16* q, const bf16* k, const bf16* v, const bf16* out,
                               const float* lse, const bf16* dout, bf16* dq, bf16* dk, bf16* dv,
                               float* delta, const DenseProblem& pb, int* status,

@@ -127,10 +127,16 @@ size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq) {
   return (size_t)B * H * Nq * sizeof(float);
 }
 
+size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int H, int Nq, int Nk, int d) {
+  if (dtype != MONARCH_DTYPE_BF16 || dense_sizes(B, H, H, Nq, Nk, d, 0, 1.f) != MONARCH_OK)
+    return 0;
+  return monarch::dense_tc_workspace_bytes(dense_problem(B, H, H, Nq, Nk, d, 0, nullptr, 1.f));
+}
+
 int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* v, void* out,
                            float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,
                            const long long* strides, int causal, const int* k_lens, float scale,
-                           cudaStream_t stream) {
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   int* launches = monarch::launch_counter();
   *launches = 0;
   if (!dtype_ok(dtype)) return MONARCH_ERR_INVALID_ARG;
@@ -145,14 +151,20 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
   const View in[3] = {{q, B, H, Nq, d, pb.q}, {k, B, Hkv, Nk, d, pb.k}, {v, B, Hkv, Nk, d, pb.v}};
   const View o = {out, B, H, Nq, d, pb.out};
   const size_t lse_bytes = (size_t)B * H * Nq * sizeof(float);
+  const size_t need = monarch_attn_dense_fwd_workspace_bytes(dtype, B, H, Nq, Nk, d);
+  if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) & 15u ||
+               workspace_bytes < need || ranges_meet(workspace, need, lse, lse_bytes)))
+    return MONARCH_ERR_INVALID_ARG;
   for (const View& x : in) {
     if (!view_ok(x, elt) || views_meet(x, o, elt)) return MONARCH_ERR_INVALID_ARG;
-    if (!x.empty() && ranges_meet(x.ptr, x.extent() * elt, lse, lse_bytes))
+    if (!x.empty() && (ranges_meet(x.ptr, x.extent() * elt, lse, lse_bytes) ||
+                       ranges_meet(x.ptr, x.extent() * elt, workspace, need)))
       return MONARCH_ERR_INVALID_ARG;
   }
   if (!view_ok(o, elt) || !distinct(o)) return MONARCH_ERR_INVALID_ARG;
   if (Nq > 0 && (!lse || reinterpret_cast<uintptr_t>(lse) % sizeof(float) ||
-                 ranges_meet(out, o.extent() * elt, lse, lse_bytes)))
+                 ranges_meet(out, o.extent() * elt, lse, lse_bytes) ||
+                 ranges_meet(out, o.extent() * elt, workspace, need)))
     return MONARCH_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return MONARCH_ERR_INVALID_ARG;
   cudaError_t e;
@@ -167,7 +179,7 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
     if ((st = status_word(&status)) != MONARCH_OK) return st;
     e = monarch::dense_tc_forward(static_cast<const bf16*>(q), static_cast<const bf16*>(k),
                                   static_cast<const bf16*>(v), static_cast<bf16*>(out), lse, pb,
-                                  status, stream, launches);
+                                  static_cast<float*>(workspace), status, stream, launches);
   } else {
     e = monarch::dense_simt_forward<bf16>(
         static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),

@@ -185,8 +185,13 @@ struct FwdLayout {
 struct FwdArgs {
   float* lse;
   DenseProblem pb;
-  int tiles;  // CTAs of a head
+  int tiles;  // CTAs along the queries of a head
   int* status;
+  // Few CTAs: the key tiles are cut into `splits` ranges of `per`, whose
+  // unnormalised results [split][b][h][i] a second launch joins in order.
+  int splits, per;
+  float2* part_mz;  // maximum in log2 units, sum
+  float* part_o;    // [d]
 };
 
 template <int D>
@@ -203,28 +208,30 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
   }
   const DenseProblem& pb = a.pb;
   // causal: the longest tiles first, over all heads; else head by head
+  const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
   int tile, bh;
   if (pb.causal) {
-    bh = blockIdx.x % (pb.B * pb.H);
-    tile = a.tiles - 1 - blockIdx.x / (pb.B * pb.H);
+    bh = unit % (pb.B * pb.H);
+    tile = a.tiles - 1 - unit / (pb.B * pb.H);
   } else {
-    tile = blockIdx.x % a.tiles;
-    bh = blockIdx.x / a.tiles;
+    tile = unit % a.tiles;
+    bh = unit / a.tiles;
   }
+  const int k0 = split * a.per * kTile;  // first key of this CTA's range
   const int h = bh % pb.H, b = bh / pb.H, hk = h / (pb.H / pb.Hkv);
   const int q0 = tile * L::kTiles * kTile;
   const int len = dense_len(pb, b);
-  // steps of the two row tiles, key tiles, and the last one's rows past the length
+  // steps of each row tile in the range, key tiles, and the last one's rows
+  // up to the length
   int nt[2] = {0, 0};
 #pragma unroll
   for (int t = 0; t < L::kTiles; ++t) {
     const int r0 = q0 + t * kTile;
-    nt[t] = r0 < pb.Nq
-                ? (dense_visible(pb, len, min(r0 + kTile, pb.Nq) - 1) + kStep - 1) / kStep
-                : 0;
+    const int keys = r0 < pb.Nq ? dense_visible(pb, len, min(r0 + kTile, pb.Nq) - 1) - k0 : 0;
+    nt[t] = min((max(keys, 0) + kStep - 1) / kStep, a.per * 2);
   }
   const int steps = max(nt[0], nt[1]), n = (steps + 1) / 2;
-  const int tail = n * kTile > len && len < pb.Nk ? len - (n - 1) * kTile : kTile;
+  const int tail = k0 + n * kTile > len && len < pb.Nk ? len - k0 - (n - 1) * kTile : kTile;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* q_full = bars;       // [2]
@@ -265,6 +272,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  pdl_launch_dependents();
 
   if (warp == L::kTmaWarp) {
     // ---- TMA: Q, then K and V tile by tile ----
@@ -284,17 +292,19 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
         const uint32_t par = (j / L::kStages - 1) & 1;
         if (j >= L::kStages && !(ok = mbar_wait(k_empty + st, par, abort_flag, a.status))) break;
         mbar_arrive_expect_tx(k_full + st, L::kTileBytes);
-        load_tile<D>(smem + L::kKOff + st * L::kTileBytes, mk, k_full + st, j * kTile, hk, b);
+        load_tile<D>(smem + L::kKOff + st * L::kTileBytes, mk, k_full + st, k0 + j * kTile, hk,
+                     b);
         kt = j + 1;
         if (j >= L::kStages && !(ok = mbar_wait(v_empty + st, par, abort_flag, a.status))) break;
         mbar_arrive_expect_tx(v_full + st, L::kTileBytes);
-        load_tile<D>(smem + L::kVOff + st * L::kTileBytes, mv, v_full + st, j * kTile, hk, b);
+        load_tile<D>(smem + L::kVOff + st * L::kTileBytes, mv, v_full + st, k0 + j * kTile, hk,
+                     b);
         vt = j + 1;
       }
     }
     __syncwarp();
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok && tail < kTile) {
+    if (ok && n > 0 && tail < kTile) {
       // values past the length may hold anything (0 x NaN): zeros in their place
       const int st = (n - 1) % L::kStages;
       if (mbar_wait(v_full + st, ((n - 1) / L::kStages) & 1, abort_flag, a.status)) {
@@ -377,8 +387,9 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
     const int nj = nt[t];
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + t * kTile + lane_off, to = tmem + L::kOCol + t * D + lane_off;
-    const int vis = dense_visible(pb, len, row);
-    const int all = dense_visible(pb, len, r0);  // keys that every row of the tile sees
+    // of the range: keys that this row, and every row of the tile, sees
+    const int vis = dense_visible(pb, len, row) - k0;
+    const int all = dense_visible(pb, len, r0) - k0;
     const float sl = pb.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl);
     float m = -INFINITY, z = 0.f;
@@ -455,7 +466,26 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
         ok = mbar_wait(s_full + 2 * t + (~nj & 1), ((nj + 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
       const bool any = vis > 0;
-      if (ok) {
+      if (ok && a.splits > 1) {
+        if (row < pb.Nq) {
+          const long at = (((long)split * pb.B + b) * pb.H + h) * pb.Nq + row;
+          a.part_mz[at] = make_float2(m * sl, any ? z : 0.f);
+        }
+        if (nj > 0) {
+          float* po = a.part_o + ((((long)split * pb.B + b) * pb.H + h) * pb.Nq + row) * pb.d;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (any && row < pb.Nq && c * 32 + e < pb.d)
+                *reinterpret_cast<float4*>(po + c * 32 + e) =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      } else if (ok) {
         accumulator_row<D>(so, r, to, 1.f / z, nj > 0, any);
         if (row < pb.Nq)
           a.lse[((long)b * pb.H + h) * pb.Nq + row] =
@@ -463,7 +493,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
         fence_proxy_async_smem();
       }
       named_barrier(1 + t, kTile);
-      if (r == 0 && ok && !*abort_flag) {
+      if (r == 0 && ok && a.splits == 1 && !*abort_flag) {
         for (int c = 0; c < L::kCh; ++c)
           if (c * 64 < pb.d) tma_store_4d(&mo.map, so + c * kChunk, c * 64, r0, h, b);
         bulk_commit();
@@ -477,6 +507,44 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+}
+
+// Joins the ranges of a split forward pass: a warp per row, the ranges
+// weighted by exp2(m - max) and summed in order.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads)
+    dense_join_kernel(bf16* __restrict__ out, FwdArgs a) {
+  pdl_wait();
+  const DenseProblem& pb = a.pb;
+  const long rows = (long)pb.B * pb.H * pb.Nq;
+  const long row = (long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  // lane = range (at most 32)
+  const float2 mz =
+      lane < a.splits ? a.part_mz[lane * rows + row] : make_float2(-INFINITY, 0.f);
+  const float m = warp_max(mz.y > 0.f ? mz.x : -INFINITY);
+  // a sum that is NaN stays: its range counts
+  const bool counts = !(mz.y == 0.f);
+  const float w = counts ? ex2(mz.x - (m == -INFINITY ? 0.f : m)) : 0.f;
+  const float z = warp_sum(counts ? w * mz.y : 0.f);
+  const bool any = __any_sync(0xffffffffu, counts);
+  const long bh = row / pb.Nq;
+  bf16* o = out + bh / pb.H * pb.out.b + bh % pb.H * pb.out.h + row % pb.Nq * pb.out.n;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) {
+    const float f = __shfl_sync(0xffffffffu, w, s);
+    if (!__shfl_sync(0xffffffffu, (int)counts, s)) continue;  // nothing was written
+    const float* p = a.part_o + (s * rows + row) * pb.d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * 32 + lane < pb.d) acc[i] = fmaf(p[i * 32 + lane], f, acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 32 + lane < pb.d) o[i * 32 + lane] = __float2bfloat16_rn(any ? acc[i] / z : 0.f);
+  if (lane == 0) a.lse[row] = any ? (m + log2f(z)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -1062,16 +1130,39 @@ bool make_tile_map(TileMap* m, const void* base, const HeadStrides& s, int B, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Ranges of the keys: as many as fill the CTA slots of the SMs (where the
+// queries alone leave half of them empty or more), of at least four tiles
+// (fewer do not pay for writing and reading a range's result), at most 32.
+template <int D>
+void split_keys(FwdArgs* a) {
+  using L = FwdLayout<D>;
+  const DenseProblem& pb = a->pb;
+  a->tiles = (pb.Nq + L::kTiles * kTile - 1) / (L::kTiles * kTile);
+  const long ctas = (long)a->tiles * pb.H * pb.B, slots = (3 - L::kTiles) * (long)num_sms();
+  const int n = (pb.Nk + kTile - 1) / kTile;
+  const int want = (int)std::max(1L, std::min({slots / std::max(1L, ctas), (long)n / 4, 32L}));
+  a->per = (n + want - 1) / want;
+  a->splits = a->per > 0 ? (n + a->per - 1) / a->per : 1;
+}
+
+void split_keys(FwdArgs* a) { a->pb.d <= 64 ? split_keys<64>(a) : split_keys<128>(a); }
+
 template <int D>
 cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mo,
-                      FwdArgs a, cudaStream_t stream, int* launches) {
+                      bf16* out, const FwdArgs& a, cudaStream_t stream, int* launches) {
   using L = FwdLayout<D>;
-  a.tiles = (a.pb.Nq + L::kTiles * kTile - 1) / (L::kTiles * kTile);
-  const cudaError_t e = allow_smem<dense_fwd_tc_kernel<D>>(L::kBytes);
+  cudaError_t e = allow_smem<dense_fwd_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)a.tiles * a.pb.H * a.pb.B;
-  return timed_launch("dense_fwd_tc", stream, launches, [&] {
+  const unsigned grid = (unsigned)a.tiles * a.pb.H * a.pb.B * a.splits;
+  e = timed_launch("dense_fwd_tc", stream, launches, [&] {
     dense_fwd_tc_kernel<D><<<grid, L::kThreads, L::kBytes, stream>>>(mq, mk, mv, mo, a);
+  });
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const long rows = (long)a.pb.B * a.pb.H * a.pb.Nq;
+  constexpr int kRows = kJoinThreads / 32;
+  return timed_launch("dense_join", stream, launches, [&] {
+    return launch_pdl(dense_join_kernel, dim3((unsigned)((rows + kRows - 1) / kRows)),
+                      dim3(kJoinThreads), 0, stream, out, a);
   });
 }
 
@@ -1105,18 +1196,36 @@ bool dense_tc_rows(const void* p, const HeadStrides& s, int N, int d) {
          s.n < kTop;
 }
 
+size_t dense_tc_workspace_bytes(const DenseProblem& pb) {
+  if (pb.d % 8 || pb.d > 128 || pb.Nq == 0 || pb.Nk == 0) return 0;
+  FwdArgs a = {};
+  a.pb = pb;
+  split_keys(&a);
+  return a.splits == 1 ? 0
+                       : (size_t)a.splits * pb.B * pb.H * pb.Nq * (pb.d + 2) * sizeof(float);
+}
+
 cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
-                             const DenseProblem& pb, int* status, cudaStream_t stream,
-                             int* launches) {
+                             const DenseProblem& pb, float* workspace, int* status,
+                             cudaStream_t stream, int* launches) {
   TileMap mq, mk, mv, mo;
   if (!make_tile_map(&mq, q, pb.q, pb.B, pb.H, pb.Nq, pb.d) ||
       !make_tile_map(&mk, k, pb.k, pb.B, pb.Hkv, pb.Nk, pb.d) ||
       !make_tile_map(&mv, v, pb.v, pb.B, pb.Hkv, pb.Nk, pb.d) ||
       !make_tile_map(&mo, out, pb.out, pb.B, pb.H, pb.Nq, pb.d))
     return cudaErrorInvalidValue;
-  FwdArgs a = {lse, pb, 0, status};
-  return pb.d <= 64 ? forward_d<64>(mq, mk, mv, mo, a, stream, launches)
-                    : forward_d<128>(mq, mk, mv, mo, a, stream, launches);
+  FwdArgs a = {};
+  a.lse = lse;
+  a.pb = pb;
+  a.status = status;
+  split_keys(&a);
+  if (a.splits > 1) {
+    a.part_o = workspace;  // (rows of d floats first: 16-byte aligned)
+    a.part_mz = reinterpret_cast<float2*>(workspace +
+                                          (size_t)a.splits * pb.B * pb.H * pb.Nq * pb.d);
+  }
+  return pb.d <= 64 ? forward_d<64>(mq, mk, mv, mo, out, a, stream, launches)
+                    : forward_d<128>(mq, mk, mv, mo, out, a, stream, launches);
 }
 
 cudaError_t dense_tc_backward(const bf16* q, const bf16* k, const bf16* v, const bf16* out,

@@ -22,9 +22,10 @@ def longs(*x):
 
 
 def fwd(lib, dtype=0, ptrs=None, sizes=(2, 4, 2, 16, 16, 64), strides=None, causal=0, lens=None,
-        scale=0.125):
+        scale=0.125, ws=10 * P, ws_bytes=1 << 24):
     ptrs = [P, 2 * P, 3 * P, 4 * P, 5 * P] if ptrs is None else ptrs
-    return lib.monarch_attn_dense_fwd(dtype, *ptrs, *sizes, strides, causal, lens, scale, None)
+    return lib.monarch_attn_dense_fwd(dtype, *ptrs, *sizes, strides, causal, lens, scale, ws,
+                                      ws_bytes, None)
 
 
 @pytest.mark.parametrize("change,expect", [
@@ -46,6 +47,10 @@ def fwd(lib, dtype=0, ptrs=None, sizes=(2, 4, 2, 16, 16, 64), strides=None, caus
     (dict(ptrs=[P, 2 * P, 3 * P, 4 * P, 2 * P]), BAD),        # lse over k
     (dict(ptrs=[P, 2 * P, 3 * P, 4 * P, 4 * P + 256]), BAD),  # lse over out
     (dict(lens=P + 2), BAD),
+    # one query over 4096 keys is split: too little workspace, none, over k
+    (dict(sizes=(1, 4, 2, 1, 4096, 64), ws_bytes=64), BAD),
+    (dict(sizes=(1, 4, 2, 1, 4096, 64), ws=None), BAD),
+    (dict(sizes=(1, 4, 2, 1, 4096, 64), ws=2 * P), BAD),
     # out with repeated elements, and a negative stride
     (dict(strides=longs(4096, 1024, 64, 2048, 1024, 64, 2048, 1024, 64, 0, 1024, 64)), BAD),
     (dict(strides=longs(4096, 1024, 64, 2048, 1024, 64, 2048, 1024, 64, 4096, 1024, 32)), BAD),
@@ -69,6 +74,9 @@ def bwd(lib, ptrs=None, sizes=(2, 4, 2, 16, 16, 64), ws=10 * P, ws_bytes=1 << 20
     dict(ptrs=[P, 2 * P, 3 * P, 4 * P, None, 6 * P, 7 * P, 8 * P, 9 * P]),
 ])
 def test_backward_refusals(lib, change):
+    assert lib.monarch_attn_dense_fwd_workspace_bytes(0, 1, 4, 1, 4096, 64) > 0
+    assert lib.monarch_attn_dense_fwd_workspace_bytes(0, 32, 12, 197, 197, 64) == 0
+    assert lib.monarch_attn_dense_fwd_workspace_bytes(1, 1, 4, 1, 4096, 64) == 0
     assert bwd(lib, **change) == BAD
     assert lib.monarch_attn_dense_bwd_workspace_bytes(2, 4, 16) == 2 * 4 * 16 * 4
     assert lib.monarch_attn_dense_bwd_workspace_bytes(0, 4, 16) == 0
@@ -88,9 +96,10 @@ def dec(lib, ptrs=None, sizes=(2, 4, 2, 64, 8, 16, 4), strides=None, scale=0.125
     (dict(sizes=(2, 4, 2, 64, 8, 0, 4)), BAD),
     (dict(sizes=(2, 4, 2, 64, 8, 1 << 20, 1 << 11)), BAD),      # more than 2^30 keys
     (dict(scale=0.0), BAD),
-    (dict(ws_bytes=16), BAD),
-    (dict(ws=None), BAD),
-    (dict(ws=2 * P), BAD),                                       # workspace over the cache
+    # 6400 keys are split: too little workspace, none, over the cache
+    (dict(sizes=(2, 4, 2, 64, 800, 16, 400), ws_bytes=16), BAD),
+    (dict(sizes=(2, 4, 2, 64, 800, 16, 400), ws=None), BAD),
+    (dict(sizes=(2, 4, 2, 64, 800, 16, 400), ws=2 * P), BAD),
     (dict(ptrs=[P, 2 * P, 3 * P, None, 5 * P, 6 * P, 7 * P]), BAD),
     (dict(ptrs=[P, 2 * P, 3 * P, 4 * P, 5 * P + 1, 6 * P, 7 * P]), BAD),
     (dict(ptrs=[P, 2 * P, 3 * P, 4 * P, 5 * P, P, 7 * P]), BAD),  # out over q

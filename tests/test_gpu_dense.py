@@ -64,6 +64,11 @@ CASES = [
     (1, 1, 1, 40, 33, 256, True, None, "head"),
     (1, 2, 2, 70, 100, 64, True, None, "odd"),              # unaligned rows
     (2, 2, 1, 520, 520, 64, True, [520, 391], "head"),      # several tiles of either axis
+    # few queries over many keys: split over the keys and joined
+    (1, 1, 1, 1, 2000, 64, False, None, "head"),
+    (2, 2, 1, 70, 2500, 128, True, [2500, 700], "token"),   # ranges that one batch never reaches
+    (1, 4, 2, 130, 1300, 80, True, None, "head"),
+    (2, 1, 1, 3, 1100, 40, False, [0, 1], "head"),
 ]
 
 
@@ -188,6 +193,24 @@ def test_repeats_are_bit_identical_and_leave_neighbours_alone(cuda_lib, dtype):
     a, b = (cuda_lib.monarch_attn_dense_bwd(q, k, v, ref, lse, do, causal=True, k_lens=kl)
             for _ in range(2))
     assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("d,H,N,causal", [(64, 40, 700, False), (128, 40, 700, True),
+                                          (64, 300, 130, True), (128, 20, 1900, False)])
+def test_more_ctas_than_the_device_holds(cuda_lib, d, H, N, causal):
+    """Waves of CTAs beside each other on an SM, softmaxes ahead of the
+    products and behind: each head as it is alone."""
+    q, k, v, do, _ = dense_case(1, H, H, N, N, d, causal, None, "head", BF16, seed=3)
+    out, lse = cuda_lib.monarch_attn_dense_fwd(q, k, v, causal=causal)
+    grads = cuda_lib.monarch_attn_dense_bwd(q, k, v, out, lse, do, causal=causal)
+    cuda_lib.check()
+    for h in (0, H // 2, H - 1):
+        x = [f64(t[:, h:h + 1]) for t in (q, k, v, do)]
+        refs = (*dense_ref.dense_forward(*x[:3], causal), *dense_ref.dense_backward(*x, causal))
+        bounds = dense_ref.dense_errors(*x, half_step(BF16), causal)
+        for name, got, ref, bound in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads),
+                                         refs, bounds):
+            close(name, got[:, h:h + 1], ref, bound)
 
 
 def test_empty_queries_and_keys(cuda_lib):
