@@ -265,22 +265,50 @@ __global__ void __launch_bounds__(4 * ROWS)
   }
 }
 
-template <typename T>
+// delta = the row sum of dO O, `lanes` (a power of two) lanes a row.  CHUNKS:
+// 16 bytes a lane at a time, four rows' in flight; else element by element.
+template <typename T, bool CHUNKS>
 __global__ void __launch_bounds__(kDeltaThreads)
     dense_delta_kernel(const T* __restrict__ out, const T* __restrict__ dout,
-                       float* __restrict__ delta, DenseProblem pb) {
-  const long row = (long)blockIdx.x * (kDeltaThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (long)pb.B * pb.H * pb.Nq) return;
-  const int i = (int)(row % pb.Nq);
-  const long bh = row / pb.Nq;
-  const int h = (int)(bh % pb.H), b = (int)(bh / pb.H);
-  const T* o = out + b * pb.out.b + h * pb.out.h + i * pb.out.n;
-  const T* g = dout + b * pb.dout.b + h * pb.dout.h + i * pb.dout.n;
-  float s = 0.f;
-  for (int c = lane; c < pb.d; c += 32) s = fmaf(to_f32(o[c]), to_f32(g[c]), s);
-  s = warp_sum(s);
-  if (lane == 0) delta[row] = s;
+                       float* __restrict__ delta, DenseProblem pb, int lanes) {
+  constexpr int E = CHUNKS ? 16 / (int)sizeof(T) : 1, kRows = 4;
+  const int per = kDeltaThreads / lanes, lane = threadIdx.x % lanes;
+  const long total = (long)pb.B * pb.H * pb.Nq;
+  const long row0 = (long)blockIdx.x * per * kRows + threadIdx.x / lanes;
+  float s[kRows];
+  const T *o[kRows], *g[kRows];
+#pragma unroll
+  for (int x = 0; x < kRows; ++x) {
+    const long row = min(row0 + x * per, total - 1);
+    const int i = (int)(row % pb.Nq), bh = (int)(row / pb.Nq), h = bh % pb.H, b = bh / pb.H;
+    o[x] = out + b * pb.out.b + h * pb.out.h + i * pb.out.n;
+    g[x] = dout + b * pb.dout.b + h * pb.dout.h + i * pb.dout.n;
+    s[x] = 0.f;
+  }
+  for (int c = lane * E; c < pb.d; c += lanes * E) {
+    if constexpr (CHUNKS) {
+      uint4 a[kRows], w[kRows];
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        a[x] = __ldg(reinterpret_cast<const uint4*>(o[x] + c));
+        w[x] = __ldg(reinterpret_cast<const uint4*>(g[x] + c));
+      }
+#pragma unroll
+      for (int x = 0; x < kRows; ++x)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          s[x] = fmaf(to_f32(reinterpret_cast<const T*>(&a[x])[e]),
+                      to_f32(reinterpret_cast<const T*>(&w[x])[e]), s[x]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) s[x] = fmaf(to_f32(o[x][c]), to_f32(g[x][c]), s[x]);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kRows; ++x) {
+    for (int y = lanes / 2; y > 0; y >>= 1) s[x] += __shfl_xor_sync(0xffffffffu, s[x], y);
+    if (lane == 0 && row0 + x * per < total) delta[row0 + x * per] = s[x];
+  }
 }
 
 // dK and dV of a tile of keys: every query head of the group and every query
@@ -538,9 +566,25 @@ cudaError_t dense_delta(const T* out, const T* dout, float* delta, const DensePr
                         cudaStream_t stream, int* launches) {
   const long rows = (long)pb.B * pb.H * pb.Nq;
   if (rows == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((rows + kDeltaThreads / 32 - 1) / (kDeltaThreads / 32));
+  constexpr int E = 16 / (int)sizeof(T);
+  bool chunks = pb.d % E == 0;
+  const void* p[2] = {out, dout};
+  const HeadStrides st[2] = {pb.out, pb.dout};
+  for (int x = 0; x < 2; ++x)
+    chunks = chunks && (reinterpret_cast<uintptr_t>(p[x]) & 15u) == 0 && st[x].b % E == 0 &&
+             st[x].h % E == 0 && st[x].n % E == 0;
+  const int units = chunks ? pb.d / E : pb.d;
+  int lanes = 1;
+  while (lanes < 32 && lanes < units) lanes *= 2;
+  const long each = kDeltaThreads / lanes * 4;
+  const unsigned blocks = (unsigned)((rows + each - 1) / each);
   return timed_launch("dense_delta", stream, launches, [&] {
-    dense_delta_kernel<T><<<blocks, kDeltaThreads, 0, stream>>>(out, dout, delta, pb);
+    if (chunks)
+      dense_delta_kernel<T, true><<<blocks, kDeltaThreads, 0, stream>>>(out, dout, delta, pb,
+                                                                        lanes);
+    else
+      dense_delta_kernel<T, false><<<blocks, kDeltaThreads, 0, stream>>>(out, dout, delta, pb,
+                                                                         lanes);
   });
 }
 

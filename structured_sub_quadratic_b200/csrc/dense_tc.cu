@@ -533,13 +533,16 @@ __global__ void __launch_bounds__(kJoinThreads)
   const long bh = row / pb.Nq;
   bf16* o = out + bh / pb.H * pb.out.b + bh % pb.H * pb.out.h + row % pb.Nq * pb.out.n;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float f = __shfl_sync(0xffffffffu, w, s);
-    if (!__shfl_sync(0xffffffffu, (int)counts, s)) continue;  // nothing was written
+    const bool written = __shfl_sync(0xffffffffu, (int)counts, s);
     const float* p = a.part_o + (s * rows + row) * pb.d;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i * 32 + lane < pb.d) acc[i] = fmaf(p[i * 32 + lane], f, acc[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float x = written && i * 32 + lane < pb.d ? p[i * 32 + lane] : 0.f;
+      acc[i] = fmaf(x, f, acc[i]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
