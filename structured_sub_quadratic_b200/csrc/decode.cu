@@ -31,13 +31,20 @@ struct Split {
   int chunks;  // chunks of the longest sequence that the table allows
 };
 
-// Four waves of two CTAs per SM over the longest sequences (ragged lengths
-// leave some empty), and 128 keys a chunk at least: fewer do not fill the
-// loads in flight of a CTA, and each chunk's result is read again by the join.
+// Chunks that fill the two CTA slots of each SM, of 128 keys at least (fewer do
+// not fill the loads in flight of a CTA).  Where a chunk is then still longer
+// than 1024 keys, up to four waves of CTAs, for lengths differ (12 to 32 waves
+// measured the same); shorter chunks lose to the start of a CTA, about 3 us (32
+// sequences of 1000 keys over 8 heads: 27 us in whole sequences, 40 us in
+// chunks of 256).  Up to 256 keys are one chunk, whose CTA writes the result
+// itself (12 heads of 250 keys: 5.8 us, in two chunks and a join 6.4; of 500
+// keys 9.1 and 6.4).
 Split make_split(const DecodeProblem& pb) {
   const long top = (long)pb.max_pages * pb.page_size;
   const long units = (long)pb.B * pb.Hkv * ((pb.H / pb.Hkv + kRows - 1) / kRows);
-  const long n = std::max(1L, std::min((top + 127) / 128, 8L * num_sms() / units));
+  long n = std::max(1L, std::min((top + 127) / 128, 2L * num_sms() / units));
+  if (top > 1024 * n) n = std::max(n, std::min((top + 1023) / 1024, 8L * num_sms() / units));
+  if (top <= 256) n = 1;
   Split s;
   s.chunk = (int)(((top + n - 1) / n + 127) / 128 * 128);
   s.chunk = std::max(s.chunk, 128);
