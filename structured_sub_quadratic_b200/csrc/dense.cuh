@@ -41,7 +41,6 @@ __device__ __forceinline__ int dense_visible(const DenseProblem& pb, int len, in
 }
 
 // CUDA-core kernels (fp32 arithmetic): every shape, stride and alignment.
-// vec: every pointer and stride allows 16-byte rows (fp32) or 8-byte (bf16).
 template <typename T>
 cudaError_t dense_simt_forward(const T* q, const T* k, const T* v, T* out, float* lse,
                                const DenseProblem& pb, cudaStream_t stream, int* launches);

@@ -43,11 +43,13 @@ __device__ __forceinline__ uint4* row_unit(uint8_t* tile, int r, int u) {
 }
 
 // 2^x of a pair on the FMA pipe, beside the exponential unit (16 results a
-// clock and SM, half of what the products of a d = 64 tile leave time for):
-// x = n + f with n the nearest integer (x + 1.5 2^23 has it in its low bits),
-// 2^f by the polynomial of least relative error on [-1/2, 1/2] (degree 5, by
-// Remez exchange: 7e-8, 2e-7 in fp32, as the unit's), n added to the exponent.
-// Below 2^-127 (hidden keys at -inf) the result is some value under 2^-125.
+// clock and SM, which a d = 64 tile keeps busier than its products do the
+// tensor cores): x = n + f with n the nearest integer (x + 1.5 2^23 has it in
+// its low bits), 2^f by the polynomial of least relative error on [-1/2, 1/2]
+// (degree 5, by Remez exchange: 7e-8, 2e-7 in fp32, as the unit's), n added to
+// the exponent.  Hidden keys, at -inf, give 2^-149, which bf16 rounds to 0 and
+// a sum does not feel; what lies between 2^-127 and 2^-126 is only known to be
+// below 2^-126.
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -127.f);
   x.y = fmaxf(x.y, -127.f);

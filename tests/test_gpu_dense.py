@@ -59,6 +59,7 @@ CASES = [
     (1, 2, 2, 33, 70, 80, True, [69], "token"),             # d between the tile widths
     (1, 3, 1, 200, 140, 40, False, None, "head"),
     (1, 2, 2, 40, 50, 24, True, None, "head"),
+    (2, 2, 1, 140, 150, 8, False, [150, 9], "token"),       # the smallest rows of 16 bytes
     (1, 1, 1, 20, 30, 7, True, None, "head"),               # d odd
     (1, 2, 1, 70, 100, 200, False, [99], "head"),           # d above the tensor-core tiles
     (1, 1, 1, 40, 33, 256, True, None, "head"),
@@ -488,6 +489,28 @@ def test_captured_graphs_are_independent(cuda_lib, dtype):
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0][5], run_all(cuda_lib, *sets[0])[5])
+    cuda_lib.check()
+
+
+def test_captured_split_forward(cuda_lib):
+    """Few queries over many keys: the ranges' workspace belongs to the graph,
+    and lengths that empty some ranges are read at replay."""
+    q, k, v, _, kl = dense_case(2, 4, 2, 5, 2600, 64, False, [2600, 2600], "head", BF16)
+    cuda_lib.monarch_attn_dense_fwd(q, k, v, k_lens=kl)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = cuda_lib.monarch_attn_dense_fwd(q, k, v, k_lens=kl)
+    for lens in ([2600, 2600], [100, 0], [2599, 1], [1400, 2600]):
+        kl.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        ref = cuda_lib.monarch_attn_dense_fwd(q, k, v, k_lens=kl)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        x = [f64(t) for t in (q, k, v)]
+        O, L = dense_ref.dense_forward(*x, lens=lens)
+        eO, eL = dense_ref.dense_errors(*x, x[0], half_step(BF16), lens=lens)[:2]
+        close("out", got[0], O, eO)
+        close("lse", got[1], L, eL)
     cuda_lib.check()
 
 
