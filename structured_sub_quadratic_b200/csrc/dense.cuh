@@ -1,5 +1,5 @@
 // Exact (dense) softmax attention: problem description and launchers shared
-// by its entry points (dense_api.cu), the CUDA-core kernels (dense_simt.cu)
+// by its entry points (dense_api.cu), the CUDA-core kernels (dense_f32.cu)
 // and the paged decode kernels (decode.cu).
 //
 //   S = scale q k^T,  P = softmax of S over the visible keys,  O = P V,
@@ -42,10 +42,10 @@ __device__ __forceinline__ int dense_visible(const DenseProblem& pb, int len, in
 
 // CUDA-core kernels (fp32 arithmetic): every shape, stride and alignment.
 template <typename T>
-cudaError_t dense_simt_forward(const T* q, const T* k, const T* v, T* out, float* lse,
+cudaError_t dense_f32_forward(const T* q, const T* k, const T* v, T* out, float* lse,
                                const DenseProblem& pb, cudaStream_t stream, int* launches);
 template <typename T>
-cudaError_t dense_simt_backward(const T* q, const T* k, const T* v, const T* out,
+cudaError_t dense_f32_backward(const T* q, const T* k, const T* v, const T* out,
                                 const float* lse, const T* dout, T* dq, T* dk, T* dv,
                                 float* delta, const DenseProblem& pb, cudaStream_t stream,
                                 int* launches);

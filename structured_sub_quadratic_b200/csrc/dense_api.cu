@@ -169,7 +169,7 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
   if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return MONARCH_ERR_INVALID_ARG;
   cudaError_t e;
   if (dtype == MONARCH_DTYPE_F32) {
-    e = monarch::dense_simt_forward<float>(
+    e = monarch::dense_f32_forward<float>(
         static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
         static_cast<float*>(out), lse, pb, stream, launches);
   } else if (Nq > 0 && Nk > 0 && monarch::dense_tc_rows(q, pb.q, Nq, d) &&
@@ -181,7 +181,7 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
                                   static_cast<const bf16*>(v), static_cast<bf16*>(out), lse, pb,
                                   static_cast<float*>(workspace), status, stream, launches);
   } else {
-    e = monarch::dense_simt_forward<bf16>(
+    e = monarch::dense_f32_forward<bf16>(
         static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),
         static_cast<bf16*>(out), lse, pb, stream, launches);
   }
@@ -240,7 +240,7 @@ int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* 
   float* delta = static_cast<float*>(workspace);
   cudaError_t e;
   if (dtype == MONARCH_DTYPE_F32) {
-    e = monarch::dense_simt_backward<float>(
+    e = monarch::dense_f32_backward<float>(
         static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
         static_cast<const float*>(out), lse, static_cast<const float*>(dout),
         static_cast<float*>(dq), static_cast<float*>(dk), static_cast<float*>(dv), delta, pb,
@@ -260,7 +260,7 @@ int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* 
     e = monarch::dense_tc_backward(bq, bk, bv, bo, lse, bg, gq, gk, gv, delta, pb, status, stream,
                                    launches);
   } else {
-    e = monarch::dense_simt_backward<bf16>(bq, bk, bv, bo, lse, bg, gq, gk, gv, delta, pb, stream,
+    e = monarch::dense_f32_backward<bf16>(bq, bk, bv, bo, lse, bg, gq, gk, gv, delta, pb, stream,
                                            launches);
   }
   return e == cudaSuccess ? MONARCH_OK : monarch::cuda_failure(e);

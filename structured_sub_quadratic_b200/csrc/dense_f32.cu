@@ -1,14 +1,24 @@
-// Exact softmax attention on the CUDA cores, forward and backward, in fp32:
-// fp32 tensors (whose bar rules out TF32), and the bf16 shapes that the
-// tensor-core kernels do not take (d above 128 or not a multiple of 8,
-// unaligned rows).
+// Exact softmax attention in fp32, forward and backward: fp32 tensors, and the
+// bf16 shapes that the tcgen05 kernels do not take (d above 128 or not a
+// multiple of 8, unaligned rows).
+//
+// The fp32 bar (1e-4 relative, 1e-6 in practice) rules out TF32 products, and
+// FFMA products were bound by shared memory at half the FFMA rate (four rows
+// by four columns a thread: one 16-byte load per eight multiply-adds).  So
+// each fp32 operand is split into two TF32 values, x = hi + lo + r with |r|
+// below 2^-21 |x|, and a product is three TF32 products, hi hi + hi lo + lo hi
+// (what is left out is below 2^-21 of it).  Tensor cores truncate their sums:
+// two steps of 8 are summed there from zero and added to the fp32 accumulator
+// in the FMA pipe, rounded to nearest.
 //
 // A CTA owns a tile of ROWS rows (queries, or keys in the dK, dV kernel) and
-// walks tiles of COLS of the other axis, both widened to fp32 in shared
-// memory.  Of its 4 ROWS threads, thread (ty, tx) holds rows ty + ROWS/4 i
-// (i < 4) and columns tx + 16 j of each score tile, and columns 4 tx + 64 c of
-// each d-wide accumulator.  Bound: the FFMA pipe, fed by float4 shared loads
-// (rows padded by 4 floats, conflict-free) in packed pairs of channels.
+// walks tiles of COLS of the other axis, both widened to fp32 in shared memory
+// (rows padded by 4 floats: fragment loads touch all banks once).  Two warps
+// share 16 rows, each with half of a tile's columns and sums of its own, which
+// are joined at the end: one warp a row block leaves an SM five warps at 12
+// heads of 1024 rows, and the kernels wait for their own instructions.  Score
+// fragments become the A operands of the second products in registers, with
+// the columns of a block of 8 in the order 0 2 4 6 1 3 5 7.
 #include "dense.cuh"
 
 #include <math.h>
@@ -35,19 +45,6 @@ __device__ __forceinline__ float4 load4<bf16>(const bf16* p) {
   const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
                      __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 v);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, float4 v) {
-  *reinterpret_cast<float4*>(p) = v;
-}
-template <>
-__device__ __forceinline__ void store4<bf16>(bf16* p, float4 v) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
 // Rows [r0, r0 + BT) of one head into shared memory as fp32, rows from n on
@@ -92,80 +89,172 @@ __device__ __forceinline__ void tiles_arrived() {
   __syncthreads();
 }
 
+// Two neighbouring channels c, c + 1 of a row.
 template <typename T>
-__device__ __forceinline__ void store_row4(T* p, float4 v, int c, int d, bool vec) {
+__device__ __forceinline__ void store_pair(T* p, float x, float y, int c, int d, bool vec) {
   if (c >= d) return;
   if (vec) {
-    store4(p + c, v);
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(p + c) = make_float2(x, y);
+    else
+      *reinterpret_cast<uint32_t*>(p + c) = tc::pack_bf16x2(x, y);
   } else {
-    p[c] = from_f32<T>(v.x);
-    if (c + 1 < d) p[c + 1] = from_f32<T>(v.y);
-    if (c + 2 < d) p[c + 2] = from_f32<T>(v.z);
-    if (c + 3 < d) p[c + 3] = from_f32<T>(v.w);
+    p[c] = from_f32<T>(x);
+    if (c + 1 < d) p[c + 1] = from_f32<T>(y);
   }
 }
 
-// acc[i][j] = A[ty + ROWS/4 i] . B[tx + 16 j] over DP channels; even and odd
-// channels are summed apart (one packed instruction for both).
-template <int ROWS, int COLS, int DP>
-__device__ __forceinline__ void scores(const float* A, const float* B, int ty, int tx,
-                                       float (&acc)[4][COLS / 16]) {
-  constexpr int J = COLS / 16, kPitch = DP + 4;
-  float2 s[4][J];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) s[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int c = 0; c < DP; c += 4) {
-    float4 a[4], b[J];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      a[i] = *reinterpret_cast<const float4*>(A + (ty + ROWS / 4 * i) * kPitch + c);
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * kPitch + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        s[i][j] = tc::fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s[i][j]);
-        s[i][j] = tc::fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s[i][j]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
+struct Split {
+  uint32_t hi, lo;
+};
+
+// hi: x cut to TF32's 11 significant bits; lo: the rest, rounded to them when
+// the product drops its last 13 bits.
+__device__ __forceinline__ Split split(float x) {
+  const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
+  return {hi, __float_as_uint(x - __uint_as_float(hi)) + 0x1000u};
 }
 
-// acc[i][c] += sum_k W[ty + ROWS/4 i][k] X[k][4 tx + 64 c ..].
-template <int ROWS, int COLS, int DP>
-__device__ __forceinline__ void accumulate(const float* W, const float* X, int ty, int tx,
-                                           float4 (&acc)[4][DP / 64]) {
-  constexpr int kPitch = DP + 4, kWPitch = COLS + 4;
-#pragma unroll 2
-  for (int k = 0; k < COLS; k += 4) {
-    float4 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = *reinterpret_cast<const float4*>(W + (ty + ROWS / 4 * i) * kWPitch + k);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-      for (int c = 0; c < DP / 64; ++c) {
-        const float4 x =
-            *reinterpret_cast<const float4*>(X + (k + kk) * kPitch + 4 * tx + 64 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-          const float2 s2 = make_float2(s, s);
-          const float2 lo = tc::fma2(s2, make_float2(x.x, x.y), make_float2(acc[i][c].x, acc[i][c].y));
-          const float2 hi = tc::fma2(s2, make_float2(x.z, x.w), make_float2(acc[i][c].z, acc[i][c].w));
-          acc[i][c] = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
-      }
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An A operand of 16 rows by 8, split.
+struct SplitA {
+  uint32_t hi[4], lo[4];
+  __device__ __forceinline__ void set(int i, float x) {
+    const Split s = split(x);
+    hi[i] = s.hi;
+    lo[i] = s.lo;
   }
+};
+
+// t[n] += A B_n for a group of blocks of B, whose two elements `b` gives:
+// product by product over all blocks, so that none waits for the one before.
+template <int kGroup, typename F>
+__device__ __forceinline__ void mma_split(float (&t)[kGroup][4], const SplitA& a, F&& b) {
+  Split s[kGroup][2];
+#pragma unroll
+  for (int n = 0; n < kGroup; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) s[n][x] = split(b(n, x));
+#pragma unroll
+  for (int n = 0; n < kGroup; ++n) mma_tf32(t[n], a.lo, s[n][0].hi, s[n][1].hi);
+#pragma unroll
+  for (int n = 0; n < kGroup; ++n) mma_tf32(t[n], a.hi, s[n][0].lo, s[n][1].lo);
+#pragma unroll
+  for (int n = 0; n < kGroup; ++n) mma_tf32(t[n], a.hi, s[n][0].hi, s[n][1].hi);
+}
+
+template <int N>
+__device__ __forceinline__ void clear(float (&acc)[N][4]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[n][x] = 0.f;
+}
+
+// acc[n] = A's 16 rows . rows 8 n .. of B, over DP channels (A: the warp's
+// first row).  A thread holds rows lane / 4 (+ 8), columns 2 (lane % 4) (+ 1).
+template <int COLS, int DP>
+__device__ __forceinline__ void scores(const float* A, const float* B, float (&acc)[COLS / 8][4]) {
+  constexpr int kPitch = DP + 4, kGroup = COLS >= 32 ? 4 : 2;
+  const int lane = threadIdx.x & 31;
+  const float* a0 = A + lane / 4 * kPitch + lane % 4;
+  const float* b0 = B + lane / 4 * kPitch + lane % 4;
+#pragma unroll
+  for (int n = 0; n < COLS / 8; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[n][x] = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < DP; c += 16) {
+    SplitA a[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[y].set(x, a0[(x & 1) * 8 * kPitch + c + y * 8 + (x >> 1) * 4]);
+#pragma unroll
+    for (int n0 = 0; n0 < COLS / 8; n0 += kGroup) {
+      float t[kGroup][4];
+      clear(t);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        mma_split(t, a[y], [&](int n, int x) {
+          return b0[(n0 + n) * 8 * kPitch + c + y * 8 + x * 4];
+        });
+#pragma unroll
+      for (int n = 0; n < kGroup; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[n0 + n][x] += t[n][x];
+    }
+  }
+}
+
+// acc[n] += W X over COLS rows of X: W as scores left it, X's channels 8 n ..
+// from `X` on.
+template <int COLS, int DP, int N>
+__device__ __forceinline__ void accumulate(const float (&w)[COLS / 8][4], const float* X,
+                                           float (&acc)[N][4]) {
+  constexpr int kPitch = DP + 4, kGroup = 4;
+  const int lane = threadIdx.x & 31;
+  const float* b0 = X + lane % 4 * 2 * kPitch + lane / 4;
+#pragma unroll
+  for (int k = 0; k < COLS / 8; k += 2) {
+    SplitA a[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      a[y].set(0, w[k + y][0]);
+      a[y].set(1, w[k + y][2]);
+      a[y].set(2, w[k + y][1]);
+      a[y].set(3, w[k + y][3]);
+    }
+#pragma unroll
+    for (int n0 = 0; n0 < N; n0 += kGroup) {
+      float t[kGroup][4];
+      clear(t);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        mma_split(t, a[y], [&](int n, int x) {
+          return b0[((k + y) * 8 + x) * kPitch + (n0 + n) * 8];
+        });
+#pragma unroll
+      for (int n = 0; n < kGroup; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[n0 + n][x] += t[n][x];
+    }
+  }
+}
+
+// A warp's 16 rows of an accumulator to shared memory, and from there.
+template <int DP, int N>
+__device__ __forceinline__ float2* pair_of(float* rows, int i, int n) {
+  const int lane = threadIdx.x & 31;
+  return reinterpret_cast<float2*>(rows + (lane / 4 + 8 * i) * (DP + 4) + n * 8 + lane % 4 * 2);
+}
+
+template <int DP, int N>
+__device__ __forceinline__ void put_rows(float* rows, const float (&acc)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      *pair_of<DP, N>(rows, i, n) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+}
+
+template <int DP, int N>
+__device__ __forceinline__ void add_rows(float* rows, float (&acc)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float2 x = *pair_of<DP, N>(rows, i, n);
+      acc[n][2 * i] += x.x;
+      acc[n][2 * i + 1] += x.y;
+    }
 }
 
 // Keys past the length may hold anything: load_tile puts zeros in their
@@ -175,13 +264,14 @@ template <typename T, int DP, int ROWS, int COLS>
 __global__ void __launch_bounds__(4 * ROWS)
     dense_fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                      T* __restrict__ out, float* __restrict__ lse, DenseProblem pb, bool vec) {
-  constexpr int J = COLS / 16, kThreads = 4 * ROWS;
+  constexpr int kThreads = 4 * ROWS, kHalf = COLS / 2, N = kHalf / 8;
   extern __shared__ __align__(16) float smf[];
   float* sQ = smf;
   float* sK = sQ + ROWS * (DP + 4);
   float* sV = sK + COLS * (DP + 4);
-  float* sP = sV + COLS * (DP + 4);  // [query][key]
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  __shared__ float other_m[ROWS], other_z[ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = warp / 2 * 16, wc = warp % 2 * kHalf;  // first row and column
   const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int q0 = (int)(blockIdx.x % tiles) * ROWS, h = bh % pb.H, b = bh / pb.H;
   const int hk = h / (pb.H / pb.Hkv);
@@ -190,78 +280,95 @@ __global__ void __launch_bounds__(4 * ROWS)
   const T* kb = k + b * pb.k.b + hk * pb.k.h;
   const T* vb = v + b * pb.v.b + hk * pb.v.h;
   load_tile<T, ROWS, DP, kThreads>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
-  int vis[4];
-  float m[4], z[4];
-  float4 o[4][DP / 64];
+  int vis[2];  // of rows lane / 4 and + 8 of the warp
+  float m[2] = {-INFINITY, -INFINITY}, z[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = q0 + ty + ROWS / 4 * i;
+  for (int i = 0; i < 2; ++i) {
+    const int row = q0 + wr + lane / 4 + 8 * i;
     vis[i] = row < pb.Nq ? dense_visible(pb, len, row) : 0;
-    m[i] = -INFINITY;
-    z[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < DP / 64; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float o[DP / 8][4];
+  clear(o);
   const int end = dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1);  // keys of the last row
   const float sl = pb.scale * kLog2e;
+#pragma unroll 1
   for (int k0 = 0; k0 < end; k0 += COLS) {
     __syncthreads();
     load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
     load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
     tiles_arrived();
-    float s[4][J];
-    scores<ROWS, COLS, DP>(sQ, sK, ty, tx, s);
+    float s[N][4];
+    scores<kHalf, DP>(sQ + wr * (DP + 4), sK + wc * (DP + 4), s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float mt = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        s[i][j] = k0 + tx + 16 * j < vis[i] ? s[i][j] * sl : -INFINITY;
-        mt = fmaxf(mt, s[i][j]);
-      }
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int x = 8; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-      const float mn = fmaxf(m[i], mt);
-      const float base = mn == -INFINITY ? 0.f : mn;
+        for (int x = 0; x < 2; ++x) {
+          float& y = s[n][2 * i + x];
+          y = k0 + wc + n * 8 + lane % 4 * 2 + x < vis[i] ? y * sl : -INFINITY;
+          mt = fmaxf(mt, y);
+        }
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
       const float corr = exp2f(m[i] - base);
-      float zt = 0.f;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const float p = exp2f(s[i][j] - base);
-        zt += p;
-        sP[(ty + ROWS / 4 * i) * (COLS + 4) + tx + 16 * j] = p;
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) zt += __shfl_xor_sync(0xffffffffu, zt, x);
-      z[i] = z[i] * corr + zt;
       m[i] = mn;
+      z[i] *= corr;
 #pragma unroll
-      for (int c = 0; c < DP / 64; ++c) {
-        o[i][c].x *= corr;
-        o[i][c].y *= corr;
-        o[i][c].z *= corr;
-        o[i][c].w *= corr;
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float& y = s[n][2 * i + x];
+          y = exp2f(y - base);
+          z[i] += y;  // this thread's keys; the row is summed at the end
+        }
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        o[n][2 * i] *= corr;
+        o[n][2 * i + 1] *= corr;
       }
     }
-    __syncthreads();
-    accumulate<ROWS, COLS, DP>(sP, sV, ty, tx, o);
+    accumulate<kHalf, DP>(s, sV + wc * (DP + 4), o);
   }
   tiles_arrived();  // (a CTA without keys still has its queries in flight)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = q0 + ty + ROWS / 4 * i;
+  for (int i = 0; i < 2; ++i) {
+    z[i] += __shfl_xor_sync(0xffffffffu, z[i], 1);
+    z[i] += __shfl_xor_sync(0xffffffffu, z[i], 2);
+  }
+  // the second warp's half of the keys, over the queries
+  float* rows = sQ + wr * (DP + 4);
+  if (wc > 0) {
+    put_rows<DP>(rows, o);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane % 4 == 0) {
+        other_m[wr + lane / 4 + 8 * i] = m[i];
+        other_z[wr + lane / 4 + 8 * i] = z[i];
+      }
+  }
+  __syncthreads();
+  if (wc > 0) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = q0 + wr + lane / 4 + 8 * i;
     if (row >= pb.Nq) continue;
-    const float inv = vis[i] > 0 ? 1.f / z[i] : 0.f;
+    const bool any = vis[i] > 0;
+    const float m1 = other_m[row - q0], mn = fmaxf(m[i], m1), base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = exp2f(m[i] - base), f1 = exp2f(m1 - base);
+    const float sum = z[i] * f0 + other_z[row - q0] * f1, inv = 1.f / sum;
     T* ob = out + b * pb.out.b + h * pb.out.h + (long)row * pb.out.n;
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) {
-      const float4 t = make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv,
-                                   o[i][c].w * inv);
-      store_row4(ob, t, 4 * tx + 64 * c, pb.d, vec);
+    for (int n = 0; n < DP / 8; ++n) {
+      const float2 p = *pair_of<DP, DP / 8>(rows, i, n);
+      const float x = (o[n][2 * i] * f0 + p.x * f1) * inv;
+      const float y = (o[n][2 * i + 1] * f0 + p.y * f1) * inv;
+      store_pair(ob, any ? x : 0.f, any ? y : 0.f, n * 8 + lane % 4 * 2, pb.d, vec);
     }
-    if (tx == 0)
-      lse[((long)b * pb.H + h) * pb.Nq + row] =
-          vis[i] > 0 ? (m[i] + log2f(z[i])) * kLn2 : -INFINITY;
+    if (lane % 4 == 0)
+      lse[((long)b * pb.H + h) * pb.Nq + row] = any ? (mn + log2f(sum)) * kLn2 : -INFINITY;
   }
 }
 
@@ -314,82 +421,97 @@ __global__ void __launch_bounds__(kDeltaThreads)
 // dK and dV of a tile of keys: every query head of the group and every query
 // tile that sees the keys, in order.
 //   P = exp(S - lse), dV = P^T dO, dS = P (dO V^T - delta), dK = scale dS^T Q
-template <typename T, int DP, int ROWS, int COLS>
+// Of 256 channels, whose two sums do not fit a warp's registers, the two warps
+// that share 16 keys take half each (CHANNELS), over all queries, instead of
+// half the queries.
+template <typename T, int DP, int ROWS, int COLS, bool CHANNELS>
 __global__ void __launch_bounds__(4 * ROWS)
     dense_dkv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                      const float* __restrict__ lse, const float* __restrict__ delta,
                      const T* __restrict__ dout, T* __restrict__ dk, T* __restrict__ dv,
                      DenseProblem pb, bool vec) {
-  constexpr int J = COLS / 16, kThreads = 4 * ROWS;
+  constexpr int kThreads = 4 * ROWS, kHalf = CHANNELS ? COLS : COLS / 2, N = kHalf / 8;
+  constexpr int kPart = CHANNELS ? DP / 2 : DP;
   extern __shared__ __align__(16) float smf[];
   float* sK = smf;
   float* sV = sK + ROWS * (DP + 4);
   float* sQ = sV + ROWS * (DP + 4);
   float* sG = sQ + COLS * (DP + 4);
-  float* sP = sG + COLS * (DP + 4);  // [key][query]
-  float* sS = sP + ROWS * (COLS + 4);
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  __shared__ float row_l2[COLS], row_dl[COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // first row, column and channel
+  const int wr = warp / 2 * 16, wc = CHANNELS ? 0 : warp % 2 * kHalf;
+  const int part = CHANNELS ? warp % 2 * kPart : 0;
   const int tiles = (pb.Nk + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int k0 = (int)(blockIdx.x % tiles) * ROWS, hk = bh % pb.Hkv, b = bh / pb.Hkv;
   const int len = dense_len(pb, b), group = pb.H / pb.Hkv;
   load_tile<T, ROWS, DP, kThreads>(sK, k + b * pb.k.b + hk * pb.k.h, pb.k.n, k0, len, pb.d, vec);
   load_tile<T, ROWS, DP, kThreads>(sV, v + b * pb.v.b + hk * pb.v.h, pb.v.n, k0, len, pb.d, vec);
-  float4 ak[4][DP / 64], av[4][DP / 64];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < DP / 64; ++c) ak[i][c] = av[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float ak[kPart / 8][4], av[kPart / 8][4];
+  clear(ak);
+  clear(av);
   // the first query that sees key k0
   const int qfirst = pb.causal ? max(0, k0 - (pb.Nk - pb.Nq)) / COLS * COLS : 0;
   const float sl = pb.scale * kLog2e;
   if (k0 < len) {
+#pragma unroll 1
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
       const T* qb = q + b * pb.q.b + h * pb.q.h;
       const T* gb = dout + b * pb.dout.b + h * pb.dout.h;
       const long row0 = ((long)b * pb.H + h) * pb.Nq;
+#pragma unroll 1
       for (int q0 = qfirst; q0 < pb.Nq; q0 += COLS) {
         __syncthreads();
         load_tile<T, COLS, DP, kThreads>(sQ, qb, pb.q.n, q0, pb.Nq, pb.d, vec);
         load_tile<T, COLS, DP, kThreads>(sG, gb, pb.dout.n, q0, pb.Nq, pb.d, vec);
-        tiles_arrived();
-        float s[4][J], dp[4][J];
-        scores<ROWS, COLS, DP>(sK, sQ, ty, tx, s);
-        scores<ROWS, COLS, DP>(sV, sG, ty, tx, dp);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int row = q0 + tx + 16 * j;
-          const bool ok = row < pb.Nq;
-          const int vis = ok ? dense_visible(pb, len, row) : 0;
-          const float l2 = ok ? __ldg(lse + row0 + row) * kLog2e : 0.f;
-          const float dl = ok ? __ldg(delta + row0 + row) : 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = ty + ROWS / 4 * i, at = key * (COLS + 4) + tx + 16 * j;
-            const bool see = k0 + key < vis;
-            const float p = see ? exp2f(fmaf(s[i][j], sl, -l2)) : 0.f;
-            sP[at] = p;
-            sS[at] = see ? p * (dp[i][j] - dl) : 0.f;
-          }
+        for (int x = threadIdx.x; x < COLS; x += kThreads) {
+          // a row outside the tensor or without keys: exp(S - inf) = 0
+          const bool live = q0 + x < pb.Nq && dense_visible(pb, len, q0 + x) > 0;
+          row_l2[x] = live ? __ldg(lse + row0 + q0 + x) * kLog2e : INFINITY;
+          row_dl[x] = live ? __ldg(delta + row0 + q0 + x) : 0.f;
         }
-        __syncthreads();
-        accumulate<ROWS, COLS, DP>(sP, sG, ty, tx, av);
-        accumulate<ROWS, COLS, DP>(sS, sQ, ty, tx, ak);
+        tiles_arrived();
+        float s[N][4], dp[N][4];
+        scores<kHalf, DP>(sK + wr * (DP + 4), sQ + wc * (DP + 4), s);
+        scores<kHalf, DP>(sV + wr * (DP + 4), sG + wc * (DP + 4), dp);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int c = wc + n * 8 + lane % 4 * 2 + (x & 1);
+            const int key = k0 + wr + lane / 4 + (x >> 1) * 8;
+            const bool see = key < dense_visible(pb, len, q0 + c);
+            const float p = see ? exp2f(fmaf(s[n][x], sl, -row_l2[c])) : 0.f;
+            s[n][x] = p;
+            dp[n][x] = see ? p * (dp[n][x] - row_dl[c]) : 0.f;
+          }
+        accumulate<kHalf, DP>(s, sG + wc * (DP + 4) + part, av);
+        accumulate<kHalf, DP>(dp, sQ + wc * (DP + 4) + part, ak);
       }
     }
   }
   tiles_arrived();
+  if constexpr (!CHANNELS) {  // the second warp's half of the queries, over K and V
+    if (wc > 0) {
+      put_rows<DP>(sK + wr * (DP + 4), ak);
+      put_rows<DP>(sV + wr * (DP + 4), av);
+    }
+    __syncthreads();
+    if (wc > 0) return;
+    add_rows<DP>(sK + wr * (DP + 4), ak);
+    add_rows<DP>(sV + wr * (DP + 4), av);
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = k0 + ty + ROWS / 4 * i;
+  for (int i = 0; i < 2; ++i) {
+    const int row = k0 + wr + lane / 4 + 8 * i;
     if (row >= pb.Nk) continue;
     T* kr = dk + b * pb.dk.b + hk * pb.dk.h + (long)row * pb.dk.n;
     T* vr = dv + b * pb.dv.b + hk * pb.dv.h + (long)row * pb.dv.n;
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) {
-      const float4 t = make_float4(ak[i][c].x * pb.scale, ak[i][c].y * pb.scale,
-                                   ak[i][c].z * pb.scale, ak[i][c].w * pb.scale);
-      store_row4(kr, t, 4 * tx + 64 * c, pb.d, vec);
-      store_row4(vr, av[i][c], 4 * tx + 64 * c, pb.d, vec);
+    for (int n = 0; n < kPart / 8; ++n) {
+      const int c = part + n * 8 + lane % 4 * 2;
+      store_pair(kr, ak[n][2 * i] * pb.scale, ak[n][2 * i + 1] * pb.scale, c, pb.d, vec);
+      store_pair(vr, av[n][2 * i], av[n][2 * i + 1], c, pb.d, vec);
     }
   }
 }
@@ -400,14 +522,14 @@ __global__ void __launch_bounds__(4 * ROWS)
     dense_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                     const float* __restrict__ lse, const float* __restrict__ delta,
                     const T* __restrict__ dout, T* __restrict__ dq, DenseProblem pb, bool vec) {
-  constexpr int J = COLS / 16, kThreads = 4 * ROWS;
+  constexpr int kThreads = 4 * ROWS, kHalf = COLS / 2, N = kHalf / 8;
   extern __shared__ __align__(16) float smf[];
   float* sQ = smf;
   float* sG = sQ + ROWS * (DP + 4);
   float* sK = sG + ROWS * (DP + 4);
   float* sV = sK + COLS * (DP + 4);
-  float* sS = sV + COLS * (DP + 4);  // [query][key]
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = warp / 2 * 16, wc = warp % 2 * kHalf;  // first row and column
   const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int q0 = (int)(blockIdx.x % tiles) * ROWS, h = bh % pb.H, b = bh / pb.H;
   const int hk = h / (pb.H / pb.Hkv);
@@ -415,54 +537,56 @@ __global__ void __launch_bounds__(4 * ROWS)
   const T* kb = k + b * pb.k.b + hk * pb.k.h;
   const T* vb = v + b * pb.v.b + hk * pb.v.h;
   load_tile<T, ROWS, DP, kThreads>(sQ, q + b * pb.q.b + h * pb.q.h, pb.q.n, q0, pb.Nq, pb.d, vec);
-  load_tile<T, ROWS, DP, kThreads>(sG, dout + b * pb.dout.b + h * pb.dout.h, pb.dout.n, q0, pb.Nq, pb.d, vec);
-  int vis[4];
-  float l2[4], dl[4];
-  float4 acc[4][DP / 64];
+  load_tile<T, ROWS, DP, kThreads>(sG, dout + b * pb.dout.b + h * pb.dout.h, pb.dout.n, q0, pb.Nq,
+                                   pb.d, vec);
+  int vis[2];
+  float l2[2], dl[2], acc[DP / 8][4];
+  clear(acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = q0 + ty + ROWS / 4 * i;
+  for (int i = 0; i < 2; ++i) {
+    const int row = q0 + wr + lane / 4 + 8 * i;
     const bool ok = row < pb.Nq;
     const long at = ((long)b * pb.H + h) * pb.Nq + row;
     vis[i] = ok ? dense_visible(pb, len, row) : 0;
     l2[i] = ok ? __ldg(lse + at) * kLog2e : 0.f;
     dl[i] = ok ? __ldg(delta + at) : 0.f;
-#pragma unroll
-    for (int c = 0; c < DP / 64; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const int end = dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1);
   const float sl = pb.scale * kLog2e;
+#pragma unroll 1
   for (int k0 = 0; k0 < end; k0 += COLS) {
     __syncthreads();
     load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
     load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
     tiles_arrived();
-    float s[4][J], dp[4][J];
-    scores<ROWS, COLS, DP>(sQ, sK, ty, tx, s);
-    scores<ROWS, COLS, DP>(sG, sV, ty, tx, dp);
+    float s[N][4], dp[N][4];
+    scores<kHalf, DP>(sQ + wr * (DP + 4), sK + wc * (DP + 4), s);
+    scores<kHalf, DP>(sG + wr * (DP + 4), sV + wc * (DP + 4), dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const bool see = k0 + tx + 16 * j < vis[i];
-        const float p = exp2f(fmaf(s[i][j], sl, -l2[i]));
-        sS[(ty + ROWS / 4 * i) * (COLS + 4) + tx + 16 * j] = see ? p * (dp[i][j] - dl[i]) : 0.f;
+      for (int x = 0; x < 4; ++x) {
+        const bool see = k0 + wc + n * 8 + lane % 4 * 2 + (x & 1) < vis[x >> 1];
+        const float p = exp2f(fmaf(s[n][x], sl, -l2[x >> 1]));
+        s[n][x] = see ? p * (dp[n][x] - dl[x >> 1]) : 0.f;
       }
-    __syncthreads();
-    accumulate<ROWS, COLS, DP>(sS, sK, ty, tx, acc);
+    accumulate<kHalf, DP>(s, sK + wc * (DP + 4), acc);
   }
   tiles_arrived();
+  // the second warp's half of the keys, over the queries
+  if (wc > 0) put_rows<DP>(sQ + wr * (DP + 4), acc);
+  __syncthreads();
+  if (wc > 0) return;
+  add_rows<DP>(sQ + wr * (DP + 4), acc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = q0 + ty + ROWS / 4 * i;
+  for (int i = 0; i < 2; ++i) {
+    const int row = q0 + wr + lane / 4 + 8 * i;
     if (row >= pb.Nq) continue;
     T* qr = dq + b * pb.dq.b + h * pb.dq.h + (long)row * pb.dq.n;
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) {
-      const float4 t = make_float4(acc[i][c].x * pb.scale, acc[i][c].y * pb.scale,
-                                   acc[i][c].z * pb.scale, acc[i][c].w * pb.scale);
-      store_row4(qr, t, 4 * tx + 64 * c, pb.d, vec);
-    }
+    for (int n = 0; n < DP / 8; ++n)
+      store_pair(qr, acc[n][2 * i] * pb.scale, acc[n][2 * i + 1] * pb.scale,
+                 n * 8 + lane % 4 * 2, pb.d, vec);
   }
 }
 
@@ -479,12 +603,12 @@ template <typename T, int DP, int ROWS, int COLS>
 cudaError_t forward_rows(const T* q, const T* k, const T* v, T* out, float* lse,
                          const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
   constexpr int smem =
-      ((ROWS + 2 * COLS) * (DP + 4) + ROWS * (COLS + 4)) * (int)sizeof(float);
+      (ROWS + 2 * COLS) * (DP + 4) * (int)sizeof(float);
   constexpr auto kernel = dense_fwd_kernel<T, DP, ROWS, COLS>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B;
-  return timed_launch("dense_fwd_simt", stream, launches, [&] {
+  return timed_launch("dense_fwd_f32", stream, launches, [&] {
     kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, out, lse, pb, vec);
   });
 }
@@ -502,12 +626,12 @@ cudaError_t dkv_rows(const T* q, const T* k, const T* v, const float* lse, const
                      const T* dout, T* dk, T* dv, const DenseProblem& pb, bool vec,
                      cudaStream_t stream, int* launches) {
   constexpr int smem =
-      (2 * (ROWS + COLS) * (DP + 4) + 2 * ROWS * (COLS + 4)) * (int)sizeof(float);
-  constexpr auto kernel = dense_dkv_kernel<T, DP, ROWS, COLS>;
+      2 * (ROWS + COLS) * (DP + 4) * (int)sizeof(float);
+  constexpr auto kernel = dense_dkv_kernel<T, DP, ROWS, COLS, (DP == 256)>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((pb.Nk + ROWS - 1) / ROWS) * pb.Hkv * pb.B;
-  return timed_launch("dense_dkv_simt", stream, launches, [&] {
+  return timed_launch("dense_dkv_f32", stream, launches, [&] {
     kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, lse, delta, dout, dk, dv, pb, vec);
   });
 }
@@ -517,12 +641,12 @@ cudaError_t dq_rows(const T* q, const T* k, const T* v, const float* lse, const 
                     const T* dout, T* dq, const DenseProblem& pb, bool vec, cudaStream_t stream,
                     int* launches) {
   constexpr int smem =
-      (2 * (ROWS + COLS) * (DP + 4) + ROWS * (COLS + 4)) * (int)sizeof(float);
+      2 * (ROWS + COLS) * (DP + 4) * (int)sizeof(float);
   constexpr auto kernel = dense_dq_kernel<T, DP, ROWS, COLS>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B;
-  return timed_launch("dense_dq_simt", stream, launches, [&] {
+  return timed_launch("dense_dq_f32", stream, launches, [&] {
     kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, lse, delta, dout, dq, pb, vec);
   });
 }
@@ -532,12 +656,13 @@ template <typename T, int DP, int TALL, int COLS>
 cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, const float* delta,
                         const T* dout, T* dq, T* dk, T* dv, const DenseProblem& pb, bool vec,
                         cudaStream_t stream, int* launches) {
+  constexpr int kSmall = DP == 64 ? COLS : 32;  // (registers of the two accumulators)
   cudaError_t e = cudaSuccess;
   if (pb.Nk > 0)
     e = few(pb.Nk, (long)pb.Hkv * pb.B)
-            ? dkv_rows<T, DP, 32, COLS>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
+            ? dkv_rows<T, DP, 32, kSmall>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
                                         launches)
-            : dkv_rows<T, DP, TALL, COLS>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
+            : dkv_rows<T, DP, TALL, kSmall>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
                                           launches);
   if (e == cudaSuccess && pb.Nq > 0)
     e = few(pb.Nq, (long)pb.H * pb.B)
@@ -550,7 +675,7 @@ cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, co
 }  // namespace
 
 template <typename T>
-cudaError_t dense_simt_forward(const T* q, const T* k, const T* v, T* out, float* lse,
+cudaError_t dense_f32_forward(const T* q, const T* k, const T* v, T* out, float* lse,
                                const DenseProblem& pb, cudaStream_t stream, int* launches) {
   if (pb.Nq == 0) return cudaSuccess;
   const bool vec = pb.d % 4 == 0 && rows_allow_four(q, pb.q, sizeof(T)) &&
@@ -589,7 +714,7 @@ cudaError_t dense_delta(const T* out, const T* dout, float* delta, const DensePr
 }
 
 template <typename T>
-cudaError_t dense_simt_backward(const T* q, const T* k, const T* v, const T* out,
+cudaError_t dense_f32_backward(const T* q, const T* k, const T* v, const T* out,
                                 const float* lse, const T* dout, T* dq, T* dk, T* dv,
                                 float* delta, const DenseProblem& pb, cudaStream_t stream,
                                 int* launches) {
@@ -610,15 +735,15 @@ cudaError_t dense_simt_backward(const T* q, const T* k, const T* v, const T* out
                                  launches);
 }
 
-template cudaError_t dense_simt_forward<float>(const float*, const float*, const float*, float*,
+template cudaError_t dense_f32_forward<float>(const float*, const float*, const float*, float*,
                                                float*, const DenseProblem&, cudaStream_t, int*);
-template cudaError_t dense_simt_forward<bf16>(const bf16*, const bf16*, const bf16*, bf16*,
+template cudaError_t dense_f32_forward<bf16>(const bf16*, const bf16*, const bf16*, bf16*,
                                               float*, const DenseProblem&, cudaStream_t, int*);
-template cudaError_t dense_simt_backward<float>(const float*, const float*, const float*,
+template cudaError_t dense_f32_backward<float>(const float*, const float*, const float*,
                                                 const float*, const float*, const float*, float*,
                                                 float*, float*, float*, const DenseProblem&,
                                                 cudaStream_t, int*);
-template cudaError_t dense_simt_backward<bf16>(const bf16*, const bf16*, const bf16*, const bf16*,
+template cudaError_t dense_f32_backward<bf16>(const bf16*, const bf16*, const bf16*, const bf16*,
                                                const float*, const bf16*, bf16*, bf16*, bf16*,
                                                float*, const DenseProblem&, cudaStream_t, int*);
 template cudaError_t dense_delta<float>(const float*, const float*, float*, const DenseProblem&,
