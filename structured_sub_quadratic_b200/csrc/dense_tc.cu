@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 // ---------------------------------------------------------------------------
 struct BwdArgs {
   const float* lse;
-  const float* delta;
+  float* delta;
   DenseProblem pb;
   int tiles;  // 128-row tiles of a head
   int* status;
@@ -877,7 +877,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // dQ of 128 queries of a head: dQ = scale sum over the key tiles of dS K,
 // dS = P (dO V^T - delta).  P stays in registers, so the next S starts as soon
 // as this one is read, and runs beside its exponentials.
-template <int D>
+// DELTA: the row sums of P (dO V^T) instead, into a.delta.
+template <int D, bool DELTA>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     dense_dq_tc_kernel(const __grid_constant__ TileMap mq, const __grid_constant__ TileMap mk,
                        const __grid_constant__ TileMap mv, const __grid_constant__ TileMap mg,
@@ -1018,7 +1019,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!(ok = warp_wait(ds_full, j & 1, abort_flag, a.status))) break;
         tc_fence_after();
-        mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol, xm + st * kStep, j > 0);
+        if (!DELTA) mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol, xm + st * kStep, j > 0);
         warp_commit(k_empty + st);
         if (more) {  // (in order: over dS once dQ has read it)
           mma_nt<D>(tmem + L::kDPCol, dg, yk + s1 * kStep);
@@ -1038,7 +1039,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const long at = ((long)b * pb.H + h) * pb.Nq + row;
     const bool live = row < pb.Nq && vis > 0;
     const float lse2 = live ? __ldg(a.lse + at) * kLog2e : INFINITY;
-    const float delta = live ? __ldg(a.delta + at) : 0.f;
+    const float delta = !DELTA && live ? __ldg(a.delta + at) : 0.f;
+    float sum = 0.f;
     const float sl = pb.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl), base2 = make_float2(-lse2, -lse2);
     const float2 nd2 = make_float2(-delta, -delta);
@@ -1072,13 +1074,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int e = 0; e < 64; ++e)
           if (e >= lim) d[e] = 0.f;
       }
-      store_half(tp, d);
-      tmem_wait_st();
+      if (DELTA) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) sum += d[e];
+      } else {
+        store_half(tp, d);
+        tmem_wait_st();
+      }
       warp_arrive(ds_full);
     }
     if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
     tc_fence_after();
-    if (half == 0) {
+    if (DELTA) {
+      float* rows = reinterpret_cast<float*>(smem + L::kRowOff);
+      if (half == 1) rows[r] = sum;
+      named_barrier(1, 2 * kTile);
+      if (half == 0 && ok && row < pb.Nq) a.delta[at] = sum + rows[r];
+    } else if (half == 0) {
       uint8_t* so = smem + L::kAOff;
       if (ok) {
         accumulator_row<D>(so, r, tmem + lane_off + L::kAccCol, pb.scale, n > 0);
@@ -1174,21 +1186,30 @@ cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, c
 template <int D>
 cudaError_t backward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mg,
                        const TileMap& mdq, const TileMap& mdk, const TileMap& mdv, BwdArgs a,
-                       cudaStream_t stream, int* launches) {
+                       bool exact_delta, cudaStream_t stream, int* launches) {
   using L = BwdLayout<D>;
-  cudaError_t e = allow_smem<dense_dkv_tc_kernel<D>>(L::kBytes);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (exact_delta) {
+    if ((e = allow_smem<dense_dq_tc_kernel<D, true>>(L::kBytes)) != cudaSuccess) return e;
+    a.tiles = (a.pb.Nq + kTile - 1) / kTile;
+    e = timed_launch("dense_delta_tc", stream, launches, [&] {
+      dense_dq_tc_kernel<D, true><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
+                                    stream>>>(mq, mk, mv, mg, mdq, a);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  if ((e = allow_smem<dense_dkv_tc_kernel<D>>(L::kBytes)) != cudaSuccess) return e;
   a.tiles = (a.pb.Nk + kTile - 1) / kTile;
   e = timed_launch("dense_dkv_tc", stream, launches, [&] {
     dense_dkv_tc_kernel<D><<<(unsigned)a.tiles * a.pb.Hkv * a.pb.B, kBwdThreads, L::kBytes,
                              stream>>>(mq, mk, mv, mg, mdk, mdv, a);
   });
   if (e != cudaSuccess) return e;
-  if ((e = allow_smem<dense_dq_tc_kernel<D>>(L::kBytes)) != cudaSuccess) return e;
+  if ((e = allow_smem<dense_dq_tc_kernel<D, false>>(L::kBytes)) != cudaSuccess) return e;
   a.tiles = (a.pb.Nq + kTile - 1) / kTile;
   return timed_launch("dense_dq_tc", stream, launches, [&] {
-    dense_dq_tc_kernel<D><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
-                            stream>>>(mq, mk, mv, mg, mdq, a);
+    dense_dq_tc_kernel<D, false><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
+                                   stream>>>(mq, mk, mv, mg, mdq, a);
   });
 }
 
@@ -1246,12 +1267,20 @@ cudaError_t dense_tc_backward(const bf16* q, const bf16* k, const bf16* v, const
       !make_tile_map(&mdk, dk, pb.dk, pb.B, pb.Hkv, pb.Nk, pb.d) ||
       !make_tile_map(&mdv, dv, pb.dv, pb.B, pb.Hkv, pb.Nk, pb.d))
     return cudaErrorInvalidValue;
-  const cudaError_t e = dense_delta<bf16>(out, dout, delta, pb, stream, launches);
-  if (e != cudaSuccess) return e;
+  // delta = row sum of dO O = row sum of P (dO V^T).  Over few keys, the bf16
+  // rounding of O in the first shows in dQ and dK (36 causal keys: error 2.8e-3
+  // of them, 2.4e-3 with the second, of which the rounding of dS and of the
+  // result are the rest); the second takes two more products, which calls of
+  // this size do not feel.
+  const bool exact_delta = pb.Nk <= 512;
+  if (!exact_delta) {
+    const cudaError_t e = dense_delta<bf16>(out, dout, delta, pb, stream, launches);
+    if (e != cudaSuccess) return e;
+  }
   const BwdArgs a = {lse, delta, pb, 0, status};
   return pb.d <= 64
-             ? backward_d<64>(mq, mk, mv, mg, mdq, mdk, mdv, a, stream, launches)
-             : backward_d<128>(mq, mk, mv, mg, mdq, mdk, mdv, a, stream, launches);
+             ? backward_d<64>(mq, mk, mv, mg, mdq, mdk, mdv, a, exact_delta, stream, launches)
+             : backward_d<128>(mq, mk, mv, mg, mdq, mdk, mdv, a, exact_delta, stream, launches);
 }
 
 }  // namespace monarch

@@ -9,7 +9,7 @@
 // Angles are far too large for 32 bits (a position of 10^6 leaves 2^-4 rad).
 // A frequency is held as a fraction of a turn in units of 2^-64, so that
 // position * frequency modulo 2^64 is the angle reduced to one turn, off by
-// 2^-34 turns for any 32-bit position; its top 32 bits go to sincospi.
+// 2^-34 turns for any 32-bit position; its top 32 bits are the angle.
 //
 // A thread keeps one place of one token (a unit: a pair, or 16-byte chunks of
 // pairs) and its cosines and sines in registers, and walks the heads of q and
@@ -36,11 +36,18 @@ constexpr int kBatch = 4;  // heads whose loads are in flight together
 //   kHalves       a chunk of first members and the chunk of their partners
 enum class Unit { kPairs, kInterleaved, kHalves };
 
-// Cosine and sine of pair r at `position`.
+// Cosine and sine of pair r at `position`.  For bf16 rows the special function
+// unit's (off by 2^-21 on [-pi, pi], a thousandth of bf16's step): with few
+// heads to share them, the angles cost more than the rows.
+template <typename T>
 __device__ __forceinline__ float2 turn(const RotaryProblem& pb, int r, int position) {
   const unsigned long long t = (unsigned long long)(long long)position * pb.turns[r];
+  const float half_turns = (float)(int)(t >> 32) * 0x1p-31f;  // in [-1, 1]
   float s, c;
-  sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);  // half turns in [-1, 1]
+  if constexpr (sizeof(T) == 2)
+    __sincosf(half_turns * 3.14159265f, &s, &c);
+  else
+    sincospif(half_turns, &s, &c);
   if (pb.inverse) s = -s;
   return make_float2(c * pb.magnitude, s * pb.magnitude);
 }
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kTurns; ++i) {
       const int c = first + 2 * i;  // a section starts at an even channel
       if (c < pb.rot) {
-        w[i] = turn(pb, c / 2, Section(pb, place, c).position);
+        w[i] = turn<T>(pb, c / 2, Section(pb, place, c).position);
         rotated = i + 1;
       }
     }
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(kThreads)
       first = pb.interleaved ? 2 * r : s.start / 2 + r;
       second = pb.interleaved ? first + 1 : first + s.half;
 #pragma unroll
-      for (int i = 0; i < kTurns; ++i) w[i] = turn(pb, r + i, s.position);
+      for (int i = 0; i < kTurns; ++i) w[i] = turn<T>(pb, r + i, s.position);
     } else {
       first = pb.rot / 2 + r;
     }
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool lead = r < s.half;
     const int at = row * pb.d + (lead ? c + s.half : c - s.half), chunk = at / E, in = at % E;
     other[i] = ((in / kPerWord) * 32 + chunk) * 4 + in % kPerWord * (int)sizeof(T);
-    w[i] = turn(pb, s.start / 2 + (lead ? r : r - s.half), s.position);
+    w[i] = turn<T>(pb, s.start / 2 + (lead ? r : r - s.half), s.position);
     if (lead) w[i].y = -w[i].y;
   }
   auto turn_chunk = [&](Chunk<T, E>& x, const uint32_t (*stage)[32]) {
