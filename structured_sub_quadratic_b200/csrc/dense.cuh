@@ -40,10 +40,30 @@ __device__ __forceinline__ int dense_visible(const DenseProblem& pb, int len, in
   return pb.causal ? max(0, min(len, i + pb.Nk - pb.Nq + 1)) : len;
 }
 
-// CUDA-core kernels (fp32 arithmetic): every shape, stride and alignment.
+// A forward pass of few CTAs cuts the keys into `splits` ranges of `per` key
+// tiles; their unnormalised results [split][b][h][i] are joined in order by a
+// second launch (dense_join.cu).
+struct KeySplit {
+  int splits = 1, per = 0;
+  float* o = nullptr;    // [d]
+  float2* mz = nullptr;  // maximum in log2 units, sum (0: no key seen, o not written)
+};
+constexpr int kMaxSplits = 32;  // a lane each in the join
+
+// n tiles of keys in ranges of at least `least` tiles, about `ctas` in all.
+KeySplit split_of(const DenseProblem& pb, int n, long have, long ctas, int least);
+size_t split_bytes(const DenseProblem& pb, const KeySplit& s);
+void place_split(const DenseProblem& pb, float* workspace, KeySplit* s);
+template <typename T>
+cudaError_t dense_join(T* out, float* lse, const DenseProblem& pb, const KeySplit& s,
+                       cudaStream_t stream, int* launches);
+
+// fp32 kernels (dense_f32.cu): every shape, stride and alignment.
+size_t dense_f32_workspace_bytes(const DenseProblem& pb);
 template <typename T>
 cudaError_t dense_f32_forward(const T* q, const T* k, const T* v, T* out, float* lse,
-                               const DenseProblem& pb, cudaStream_t stream, int* launches);
+                              const DenseProblem& pb, float* workspace, cudaStream_t stream,
+                              int* launches);
 template <typename T>
 cudaError_t dense_f32_backward(const T* q, const T* k, const T* v, const T* out,
                                 const float* lse, const T* dout, T* dq, T* dk, T* dv,

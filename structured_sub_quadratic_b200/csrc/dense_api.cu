@@ -128,9 +128,12 @@ size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq) {
 }
 
 size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int H, int Nq, int Nk, int d) {
-  if (dtype != MONARCH_DTYPE_BF16 || dense_sizes(B, H, H, Nq, Nk, d, 0, 1.f) != MONARCH_OK)
-    return 0;
-  return monarch::dense_tc_workspace_bytes(dense_problem(B, H, H, Nq, Nk, d, 0, nullptr, 1.f));
+  if (!dtype_ok(dtype) || dense_sizes(B, H, H, Nq, Nk, d, 0, 1.f) != MONARCH_OK) return 0;
+  const DenseProblem pb = dense_problem(B, H, H, Nq, Nk, d, 0, nullptr, 1.f);
+  // (which kernels take bf16 tensors depends on their alignment, too)
+  const size_t f32 = monarch::dense_f32_workspace_bytes(pb);
+  const size_t tc = dtype == MONARCH_DTYPE_BF16 ? monarch::dense_tc_workspace_bytes(pb) : 0;
+  return f32 > tc ? f32 : tc;
 }
 
 int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* v, void* out,
@@ -171,7 +174,7 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
   if (dtype == MONARCH_DTYPE_F32) {
     e = monarch::dense_f32_forward<float>(
         static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
-        static_cast<float*>(out), lse, pb, stream, launches);
+        static_cast<float*>(out), lse, pb, static_cast<float*>(workspace), stream, launches);
   } else if (Nq > 0 && Nk > 0 && monarch::dense_tc_rows(q, pb.q, Nq, d) &&
              monarch::dense_tc_rows(k, pb.k, Nk, d) && monarch::dense_tc_rows(v, pb.v, Nk, d) &&
              monarch::dense_tc_rows(out, pb.out, Nq, d)) {
@@ -183,7 +186,7 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
   } else {
     e = monarch::dense_f32_forward<bf16>(
         static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),
-        static_cast<bf16*>(out), lse, pb, stream, launches);
+        static_cast<bf16*>(out), lse, pb, static_cast<float*>(workspace), stream, launches);
   }
   return e == cudaSuccess ? MONARCH_OK : monarch::cuda_failure(e);
 }

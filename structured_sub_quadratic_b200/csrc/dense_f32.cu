@@ -263,7 +263,8 @@ __device__ __forceinline__ void add_rows(float* rows, float (&acc)[N][4]) {
 template <typename T, int DP, int ROWS, int COLS>
 __global__ void __launch_bounds__(4 * ROWS)
     dense_fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                     T* __restrict__ out, float* __restrict__ lse, DenseProblem pb, bool vec) {
+                     T* __restrict__ out, float* __restrict__ lse, DenseProblem pb, KeySplit split,
+                     bool vec) {
   constexpr int kThreads = 4 * ROWS, kHalf = COLS / 2, N = kHalf / 8;
   extern __shared__ __align__(16) float smf[];
   float* sQ = smf;
@@ -272,8 +273,10 @@ __global__ void __launch_bounds__(4 * ROWS)
   __shared__ float other_m[ROWS], other_z[ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp / 2 * 16, wc = warp % 2 * kHalf;  // first row and column
-  const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
-  const int q0 = (int)(blockIdx.x % tiles) * ROWS, h = bh % pb.H, b = bh / pb.H;
+  tc::pdl_launch_dependents();
+  const int range = blockIdx.x % split.splits, unit = blockIdx.x / split.splits;
+  const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = unit / tiles;
+  const int q0 = unit % tiles * ROWS, h = bh % pb.H, b = bh / pb.H;
   const int hk = h / (pb.H / pb.Hkv);
   const int len = dense_len(pb, b);
   const T* qb = q + b * pb.q.b + h * pb.q.h;
@@ -289,10 +292,12 @@ __global__ void __launch_bounds__(4 * ROWS)
   }
   float o[DP / 8][4];
   clear(o);
-  const int end = dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1);  // keys of the last row
+  // keys of the range that the last row sees
+  const int first = range * split.per * COLS;
+  const int end = min(dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1), first + split.per * COLS);
   const float sl = pb.scale * kLog2e;
 #pragma unroll 1
-  for (int k0 = 0; k0 < end; k0 += COLS) {
+  for (int k0 = first; k0 < end; k0 += COLS) {
     __syncthreads();
     load_tile<T, COLS, DP, kThreads>(sK, kb, pb.k.n, k0, len, pb.d, vec);
     load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
@@ -355,20 +360,30 @@ __global__ void __launch_bounds__(4 * ROWS)
   for (int i = 0; i < 2; ++i) {
     const int row = q0 + wr + lane / 4 + 8 * i;
     if (row >= pb.Nq) continue;
-    const bool any = vis[i] > 0;
+    const bool any = vis[i] > first;
     const float m1 = other_m[row - q0], mn = fmaxf(m[i], m1), base = mn == -INFINITY ? 0.f : mn;
     const float f0 = exp2f(m[i] - base), f1 = exp2f(m1 - base);
-    const float sum = z[i] * f0 + other_z[row - q0] * f1, inv = 1.f / sum;
+    const float sum = z[i] * f0 + other_z[row - q0] * f1;
+    const bool whole = split.splits == 1;
+    const float inv = whole ? 1.f / sum : 1.f;
+    const long at = (((long)range * pb.B + b) * pb.H + h) * pb.Nq + row;
     T* ob = out + b * pb.out.b + h * pb.out.h + (long)row * pb.out.n;
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n) {
       const float2 p = *pair_of<DP, DP / 8>(rows, i, n);
       const float x = (o[n][2 * i] * f0 + p.x * f1) * inv;
       const float y = (o[n][2 * i + 1] * f0 + p.y * f1) * inv;
-      store_pair(ob, any ? x : 0.f, any ? y : 0.f, n * 8 + lane % 4 * 2, pb.d, vec);
+      const int c = n * 8 + lane % 4 * 2;
+      if (whole)
+        store_pair(ob, any ? x : 0.f, any ? y : 0.f, c, pb.d, vec);
+      else if (any)
+        store_pair(split.o + at * pb.d, x, y, c, pb.d, pb.d % 4 == 0);
     }
-    if (lane % 4 == 0)
+    if (lane % 4) continue;
+    if (whole)
       lse[((long)b * pb.H + h) * pb.Nq + row] = any ? (mn + log2f(sum)) * kLn2 : -INFINITY;
+    else
+      split.mz[at] = make_float2(mn, any ? sum : 0.f);
   }
 }
 
@@ -599,26 +614,40 @@ bool rows_allow_four(const void* p, const HeadStrides& s, size_t elt) {
 // leave the SMs fewer than four CTAs each.
 inline bool few(long rows, long heads) { return (rows + 63) / 64 * heads < 4L * num_sms(); }
 
-template <typename T, int DP, int ROWS, int COLS>
+// Keys of a tile of the forward pass.
+constexpr int fwd_cols(int d) { return d <= 128 ? 64 : 32; }
+
+// Ranges of at least two tiles, up to four CTAs of 32 queries per SM.
+KeySplit split_keys(const DenseProblem& pb) {
+  const int cols = fwd_cols(pb.d);
+  const long ctas = (long)((pb.Nq + 31) / 32) * pb.H * pb.B;
+  return split_of(pb, (pb.Nk + cols - 1) / cols, ctas, 4L * num_sms(), 2);
+}
+
+template <typename T, int DP, int ROWS>
 cudaError_t forward_rows(const T* q, const T* k, const T* v, T* out, float* lse,
-                         const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
-  constexpr int smem =
-      (ROWS + 2 * COLS) * (DP + 4) * (int)sizeof(float);
+                         const DenseProblem& pb, const KeySplit& split, bool vec,
+                         cudaStream_t stream, int* launches) {
+  constexpr int COLS = fwd_cols(DP);
+  constexpr int smem = (ROWS + 2 * COLS) * (DP + 4) * (int)sizeof(float);
   constexpr auto kernel = dense_fwd_kernel<T, DP, ROWS, COLS>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B;
-  return timed_launch("dense_fwd_f32", stream, launches, [&] {
-    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, out, lse, pb, vec);
+  const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B * split.splits;
+  e = timed_launch("dense_fwd_f32", stream, launches, [&] {
+    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, out, lse, pb, split, vec);
   });
+  if (e != cudaSuccess || split.splits == 1) return e;
+  return dense_join<T>(out, lse, pb, split, stream, launches);
 }
 
-template <typename T, int DP, int COLS>
+template <typename T, int DP>
 cudaError_t forward_dp(const T* q, const T* k, const T* v, T* out, float* lse,
-                       const DenseProblem& pb, bool vec, cudaStream_t stream, int* launches) {
+                       const DenseProblem& pb, const KeySplit& split, bool vec,
+                       cudaStream_t stream, int* launches) {
   return few(pb.Nq, (long)pb.H * pb.B)
-             ? forward_rows<T, DP, 32, COLS>(q, k, v, out, lse, pb, vec, stream, launches)
-             : forward_rows<T, DP, 64, COLS>(q, k, v, out, lse, pb, vec, stream, launches);
+             ? forward_rows<T, DP, 32>(q, k, v, out, lse, pb, split, vec, stream, launches)
+             : forward_rows<T, DP, 64>(q, k, v, out, lse, pb, split, vec, stream, launches);
 }
 
 template <typename T, int DP, int ROWS, int COLS>
@@ -674,16 +703,24 @@ cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, co
 
 }  // namespace
 
+size_t dense_f32_workspace_bytes(const DenseProblem& pb) {
+  return pb.Nq == 0 ? 0 : split_bytes(pb, split_keys(pb));
+}
+
 template <typename T>
 cudaError_t dense_f32_forward(const T* q, const T* k, const T* v, T* out, float* lse,
-                               const DenseProblem& pb, cudaStream_t stream, int* launches) {
+                              const DenseProblem& pb, float* workspace, cudaStream_t stream,
+                              int* launches) {
   if (pb.Nq == 0) return cudaSuccess;
   const bool vec = pb.d % 4 == 0 && rows_allow_four(q, pb.q, sizeof(T)) &&
                    rows_allow_four(k, pb.k, sizeof(T)) && rows_allow_four(v, pb.v, sizeof(T)) &&
                    rows_allow_four(out, pb.out, sizeof(T));
-  if (pb.d <= 64) return forward_dp<T, 64, 64>(q, k, v, out, lse, pb, vec, stream, launches);
-  if (pb.d <= 128) return forward_dp<T, 128, 64>(q, k, v, out, lse, pb, vec, stream, launches);
-  return forward_dp<T, 256, 32>(q, k, v, out, lse, pb, vec, stream, launches);
+  KeySplit split = split_keys(pb);
+  place_split(pb, workspace, &split);
+  const auto forward = pb.d <= 64    ? forward_dp<T, 64>
+                       : pb.d <= 128 ? forward_dp<T, 128>
+                                     : forward_dp<T, 256>;
+  return forward(q, k, v, out, lse, pb, split, vec, stream, launches);
 }
 
 template <typename T>
@@ -735,10 +772,10 @@ cudaError_t dense_f32_backward(const T* q, const T* k, const T* v, const T* out,
                                  launches);
 }
 
-template cudaError_t dense_f32_forward<float>(const float*, const float*, const float*, float*,
-                                               float*, const DenseProblem&, cudaStream_t, int*);
-template cudaError_t dense_f32_forward<bf16>(const bf16*, const bf16*, const bf16*, bf16*,
-                                              float*, const DenseProblem&, cudaStream_t, int*);
+template cudaError_t dense_f32_forward<float>(const float*, const float*, const float*, float*, float*,
+                                              const DenseProblem&, float*, cudaStream_t, int*);
+template cudaError_t dense_f32_forward<bf16>(const bf16*, const bf16*, const bf16*, bf16*, float*,
+                                              const DenseProblem&, float*, cudaStream_t, int*);
 template cudaError_t dense_f32_backward<float>(const float*, const float*, const float*,
                                                 const float*, const float*, const float*, float*,
                                                 float*, float*, float*, const DenseProblem&,

@@ -189,11 +189,7 @@ struct FwdArgs {
   DenseProblem pb;
   int tiles;  // CTAs along the queries of a head
   int* status;
-  // Few CTAs: the key tiles are cut into `splits` ranges of `per`, whose
-  // unnormalised results [split][b][h][i] a second launch joins in order.
-  int splits, per;
-  float2* part_mz;  // maximum in log2 units, sum
-  float* part_o;    // [d]
+  KeySplit split;
 };
 
 template <int D>
@@ -210,7 +206,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
   }
   const DenseProblem& pb = a.pb;
   // causal: the longest tiles first, over all heads; else head by head
-  const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.split.splits, unit = blockIdx.x / a.split.splits;
   int tile, bh;
   if (pb.causal) {
     bh = unit % (pb.B * pb.H);
@@ -219,7 +215,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
     tile = unit % a.tiles;
     bh = unit / a.tiles;
   }
-  const int k0 = split * a.per * kTile;  // first key of this CTA's range
+  const int k0 = split * a.split.per * kTile;  // first key of this CTA's range
   const int h = bh % pb.H, b = bh / pb.H, hk = h / (pb.H / pb.Hkv);
   const int q0 = tile * L::kTiles * kTile;
   const int len = dense_len(pb, b);
@@ -230,7 +226,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
   for (int t = 0; t < L::kTiles; ++t) {
     const int r0 = q0 + t * kTile;
     const int keys = r0 < pb.Nq ? dense_visible(pb, len, min(r0 + kTile, pb.Nq) - 1) - k0 : 0;
-    nt[t] = min((max(keys, 0) + kStep - 1) / kStep, a.per * 2);
+    nt[t] = min((max(keys, 0) + kStep - 1) / kStep, a.split.per * 2);
   }
   const int steps = max(nt[0], nt[1]), n = (steps + 1) / 2;
   const int tail = k0 + n * kTile > len && len < pb.Nk ? len - k0 - (n - 1) * kTile : kTile;
@@ -468,13 +464,13 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
         ok = mbar_wait(s_full + 2 * t + (~nj & 1), ((nj + 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
       const bool any = vis > 0;
-      if (ok && a.splits > 1) {
+      if (ok && a.split.splits > 1) {
         if (row < pb.Nq) {
           const long at = (((long)split * pb.B + b) * pb.H + h) * pb.Nq + row;
-          a.part_mz[at] = make_float2(m * sl, any ? z : 0.f);
+          a.split.mz[at] = make_float2(m * sl, any ? z : 0.f);
         }
         if (nj > 0) {
-          float* po = a.part_o + ((((long)split * pb.B + b) * pb.H + h) * pb.Nq + row) * pb.d;
+          float* po = a.split.o + ((((long)split * pb.B + b) * pb.H + h) * pb.Nq + row) * pb.d;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
@@ -495,7 +491,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
         fence_proxy_async_smem();
       }
       named_barrier(1 + t, kTile);
-      if (r == 0 && ok && a.splits == 1 && !*abort_flag) {
+      if (r == 0 && ok && a.split.splits == 1 && !*abort_flag) {
         for (int c = 0; c < L::kCh; ++c)
           if (c * 64 < pb.d) tma_store_4d(&mo.map, so + c * kChunk, c * 64, r0, h, b);
         bulk_commit();
@@ -509,47 +505,6 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
-}
-
-// Joins the ranges of a split forward pass: a warp per row, the ranges
-// weighted by exp2(m - max) and summed in order.
-constexpr int kJoinThreads = 256;
-
-__global__ void __launch_bounds__(kJoinThreads)
-    dense_join_kernel(bf16* __restrict__ out, FwdArgs a) {
-  pdl_wait();
-  const DenseProblem& pb = a.pb;
-  const long rows = (long)pb.B * pb.H * pb.Nq;
-  const long row = (long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  // lane = range (at most 32)
-  const float2 mz =
-      lane < a.splits ? a.part_mz[lane * rows + row] : make_float2(-INFINITY, 0.f);
-  const float m = warp_max(mz.y > 0.f ? mz.x : -INFINITY);
-  // a sum that is NaN stays: its range counts
-  const bool counts = !(mz.y == 0.f);
-  const float w = counts ? ex2(mz.x - (m == -INFINITY ? 0.f : m)) : 0.f;
-  const float z = warp_sum(counts ? w * mz.y : 0.f);
-  const bool any = __any_sync(0xffffffffu, counts);
-  const long bh = row / pb.Nq;
-  bf16* o = out + bh / pb.H * pb.out.b + bh % pb.H * pb.out.h + row % pb.Nq * pb.out.n;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = __shfl_sync(0xffffffffu, w, s);
-    const bool written = __shfl_sync(0xffffffffu, (int)counts, s);
-    const float* p = a.part_o + (s * rows + row) * pb.d;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = written && i * 32 + lane < pb.d ? p[i * 32 + lane] : 0.f;
-      acc[i] = fmaf(x, f, acc[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i * 32 + lane < pb.d) o[i * 32 + lane] = __float2bfloat16_rn(any ? acc[i] / z : 0.f);
-  if (lane == 0) a.lse[row] = any ? (m + log2f(z)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -1148,39 +1103,27 @@ bool make_tile_map(TileMap* m, const void* base, const HeadStrides& s, int B, in
 }
 
 // Ranges of the keys: as many as fill the CTA slots of the SMs (where the
-// queries alone leave half of them empty or more), of at least four tiles
-// (fewer do not pay for writing and reading a range's result), at most 32.
-template <int D>
-void split_keys(FwdArgs* a) {
-  using L = FwdLayout<D>;
-  const DenseProblem& pb = a->pb;
-  a->tiles = (pb.Nq + L::kTiles * kTile - 1) / (L::kTiles * kTile);
-  const long ctas = (long)a->tiles * pb.H * pb.B, slots = (3 - L::kTiles) * (long)num_sms();
-  const int n = (pb.Nk + kTile - 1) / kTile;
-  const int want = (int)std::max(1L, std::min({slots / std::max(1L, ctas), (long)n / 4, 32L}));
-  a->per = (n + want - 1) / want;
-  a->splits = a->per > 0 ? (n + a->per - 1) / a->per : 1;
+// queries alone leave half of them empty or more), of at least four tiles:
+// fewer do not pay for writing and reading a range's result.
+KeySplit split_keys(const DenseProblem& pb) {
+  const int tiles = pb.d <= 64 ? FwdLayout<64>::kTiles : FwdLayout<128>::kTiles;
+  const long ctas = (long)((pb.Nq + tiles * kTile - 1) / (tiles * kTile)) * pb.H * pb.B;
+  return split_of(pb, (pb.Nk + kTile - 1) / kTile, ctas, (3 - tiles) * (long)num_sms(), 4);
 }
-
-void split_keys(FwdArgs* a) { a->pb.d <= 64 ? split_keys<64>(a) : split_keys<128>(a); }
 
 template <int D>
 cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mo,
-                      bf16* out, const FwdArgs& a, cudaStream_t stream, int* launches) {
+                      bf16* out, FwdArgs a, cudaStream_t stream, int* launches) {
   using L = FwdLayout<D>;
   cudaError_t e = allow_smem<dense_fwd_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)a.tiles * a.pb.H * a.pb.B * a.splits;
+  a.tiles = (a.pb.Nq + L::kTiles * kTile - 1) / (L::kTiles * kTile);
+  const unsigned grid = (unsigned)a.tiles * a.pb.H * a.pb.B * a.split.splits;
   e = timed_launch("dense_fwd_tc", stream, launches, [&] {
     dense_fwd_tc_kernel<D><<<grid, L::kThreads, L::kBytes, stream>>>(mq, mk, mv, mo, a);
   });
-  if (e != cudaSuccess || a.splits == 1) return e;
-  const long rows = (long)a.pb.B * a.pb.H * a.pb.Nq;
-  constexpr int kRows = kJoinThreads / 32;
-  return timed_launch("dense_join", stream, launches, [&] {
-    return launch_pdl(dense_join_kernel, dim3((unsigned)((rows + kRows - 1) / kRows)),
-                      dim3(kJoinThreads), 0, stream, out, a);
-  });
+  if (e != cudaSuccess || a.split.splits == 1) return e;
+  return dense_join<bf16>(out, a.lse, a.pb, a.split, stream, launches);
 }
 
 template <int D>
@@ -1224,11 +1167,7 @@ bool dense_tc_rows(const void* p, const HeadStrides& s, int N, int d) {
 
 size_t dense_tc_workspace_bytes(const DenseProblem& pb) {
   if (pb.d % 8 || pb.d > 128 || pb.Nq == 0 || pb.Nk == 0) return 0;
-  FwdArgs a = {};
-  a.pb = pb;
-  split_keys(&a);
-  return a.splits == 1 ? 0
-                       : (size_t)a.splits * pb.B * pb.H * pb.Nq * (pb.d + 2) * sizeof(float);
+  return split_bytes(pb, split_keys(pb));
 }
 
 cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* out, float* lse,
@@ -1244,12 +1183,8 @@ cudaError_t dense_tc_forward(const bf16* q, const bf16* k, const bf16* v, bf16* 
   a.lse = lse;
   a.pb = pb;
   a.status = status;
-  split_keys(&a);
-  if (a.splits > 1) {
-    a.part_o = workspace;  // (rows of d floats first: 16-byte aligned)
-    a.part_mz = reinterpret_cast<float2*>(workspace +
-                                          (size_t)a.splits * pb.B * pb.H * pb.Nq * pb.d);
-  }
+  a.split = split_keys(pb);
+  place_split(pb, workspace, &a.split);
   return pb.d <= 64 ? forward_d<64>(mq, mk, mv, mo, out, a, stream, launches)
                     : forward_d<128>(mq, mk, mv, mo, out, a, stream, launches);
 }

@@ -76,7 +76,8 @@ def bwd(lib, ptrs=None, sizes=(2, 4, 2, 16, 16, 64), ws=10 * P, ws_bytes=1 << 20
 def test_backward_refusals(lib, change):
     assert lib.monarch_attn_dense_fwd_workspace_bytes(0, 1, 4, 1, 4096, 64) > 0
     assert lib.monarch_attn_dense_fwd_workspace_bytes(0, 32, 12, 197, 197, 64) == 0
-    assert lib.monarch_attn_dense_fwd_workspace_bytes(1, 1, 4, 1, 4096, 64) == 0
+    assert lib.monarch_attn_dense_fwd_workspace_bytes(1, 1, 4, 1, 4096, 64) > 0
+    assert lib.monarch_attn_dense_fwd_workspace_bytes(1, 1, 4, 1, 64, 64) == 0
     assert bwd(lib, **change) == BAD
     assert lib.monarch_attn_dense_bwd_workspace_bytes(2, 4, 16) == 2 * 4 * 16 * 4
     assert lib.monarch_attn_dense_bwd_workspace_bytes(0, 4, 16) == 0
