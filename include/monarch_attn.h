@@ -265,7 +265,9 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
  * A row without a visible key gets out = 0 and lse = -inf.  Keys past the
  * length may hold anything (NaN included); keys hidden by `causal` alone must
  * be finite.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
- * for the product with v, sums are fp32.  scale > 0.  Few queries over many
+ * for the product with v, sums are fp32.  fp32: operands are split into two
+ * TF32 values and a product is off by 2^-20 of it at most; an infinity among
+ * the visible values gives NaN.  scale > 0.  Few queries over many
  * keys are split over the keys and joined in order; workspace: device,
  * 16-byte aligned, monarch_attn_dense_fwd_workspace_bytes (0 where nothing is
  * split). */

@@ -308,15 +308,15 @@ def _int_tensor(name, t, like, shape):
     return t.data_ptr()
 
 
-_STRIDES = {n: _L * (3 * n) for n in (4, 8)}
+@functools.lru_cache(maxsize=256)
+def _stride_array(*strides):
+    """Batch, head and token strides, tensor after tensor, for the C ABI."""
+    flat = [x for s in strides for x in s[:3]]
+    return (_L * len(flat))(*flat)
 
 
 def _strides(*tensors):
-    """Batch, head and token strides of (B, H, N, d) tensors for the C ABI."""
-    flat = []
-    for t in tensors:
-        flat += t.stride()[:3]
-    return _STRIDES[len(tensors)](*flat)
+    return _stride_array(*(t.stride() for t in tensors))
 
 
 @functools.lru_cache(maxsize=256)
@@ -442,8 +442,8 @@ def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None,
     need = _workspace_need("dense_decode", q.get_device(), dtype, B, H, Hkv, d, page_size,
                            max_pages)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    strides = _STRIDES[4](*q.stride()[:2], 0, *k_cache.stride()[:3], *v_cache.stride()[:3],
-                          *out.stride()[:2], 0)
+    # (a query's and an output's third stride, of one token, is not used)
+    strides = _strides(q, k_cache, v_cache, out)
     _check(lib.monarch_attn_dense_decode(
         dtype, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, len_ptr,
         out.data_ptr(), lse.data_ptr(), B, H, Hkv, d, pages, page_size, max_pages, strides,
@@ -489,9 +489,13 @@ def rotary_frequencies(axis_dims, base=10000.0, scaling=None):
 
 @functools.lru_cache(maxsize=64)
 def _rotary_args(axis_dims, base, scaling):
-    """ctypes forms of axis_dims and the frequencies (a function of the arguments alone)."""
+    """ctypes forms of axis_dims and the frequencies, and the rotated channels
+    (a function of the arguments alone)."""
+    if not 1 <= len(axis_dims) <= 4 or any(n < 2 or n % 2 for n in axis_dims):
+        raise ValueError("axis_dims must be one to four even sizes")
     freqs, magnitude = rotary_frequencies(axis_dims, base, scaling)
-    return ((_I * len(axis_dims))(*axis_dims), (_D * len(freqs))(*freqs), magnitude)
+    return ((_I * len(axis_dims))(*axis_dims), (_D * len(freqs))(*freqs), magnitude,
+            sum(axis_dims))
 
 
 def monarch_attn_rotary(q, k=None, positions=None, *, axis_dims=None, grid=None,
@@ -516,9 +520,10 @@ def monarch_attn_rotary(q, k=None, positions=None, *, axis_dims=None, grid=None,
         raise ValueError("expected q (B, H, N, d) and k (B, Hkv, N, d)")
     B, H, N, d = q.shape
     axis_dims = (d,) if axis_dims is None else tuple(axis_dims)
-    if not 1 <= len(axis_dims) <= 4 or any(n < 2 or n % 2 for n in axis_dims) \
-            or sum(axis_dims) > d:
-        raise ValueError("axis_dims must be one to four even sizes within d channels")
+    dims, freqs, magnitude, rotated = _rotary_args(
+        axis_dims, base, None if scaling is None else tuple(scaling))
+    if rotated > d:
+        raise ValueError(f"axis_dims rotate {rotated} of {d} channels")
     given = [t for t in (k, q_out, k_out) if t is not None]
     dtype = _dense_dtype("q, k and the outputs", q, *given)
     if (q_out is not None and q_out.shape != q.shape) or \
@@ -543,7 +548,6 @@ def monarch_attn_rotary(q, k=None, positions=None, *, axis_dims=None, grid=None,
             return monarch_attn_rotary(q, k, positions, axis_dims=axis_dims, grid=grid,
                                        interleaved=interleaved, base=base, scaling=scaling,
                                        inverse=inverse, q_out=q_out, k_out=k_out)
-    dims, freqs, magnitude = _rotary_args(axis_dims, base, scaling)
     if q_out is None:
         q_out = _like(q)
     if k is None:
