@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads)
   using L = MmaTile<DP>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sm[kWarps][kRows], sz[kWarps][kRows];
-  tc::pdl_launch_dependents();
+  if (sp.chunks > 1) tc::pdl_launch_dependents();  // the join
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Share s = share_of(pb, sp, kRows, status);
   if (s.j0 >= s.j1) {  // the join reads no chunk from the length on
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads)
   static_assert(kVals <= 32 && (kVals & (kVals - 1)) == 0, "dot products of a tile");
   __shared__ float sm[kWarps][kRows], sz[kWarps][kRows];
   __shared__ float so[kWarps][GH][DP + 4];
-  tc::pdl_launch_dependents();
+  if (sp.chunks > 1) tc::pdl_launch_dependents();  // the join
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * CH;
   const Share s = share_of(pb, sp, GH, status);
   if (s.j0 >= s.j1) {

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(4 * ROWS)
   __shared__ float other_m[ROWS], other_z[ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp / 2 * 16, wc = warp % 2 * kHalf;  // first row and column
-  tc::pdl_launch_dependents();
+  if (split.splits > 1) tc::pdl_launch_dependents();  // the join
   const int range = blockIdx.x % split.splits, unit = blockIdx.x / split.splits;
   const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = unit / tiles;
   const int q0 = unit % tiles * ROWS, h = bh % pb.H, b = bh / pb.H;

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  pdl_launch_dependents();
+  if (a.split.splits > 1) pdl_launch_dependents();  // the join
 
   if (warp == L::kTmaWarp) {
     // ---- TMA: Q, then K and V tile by tile ----

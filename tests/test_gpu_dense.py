@@ -526,3 +526,24 @@ def test_calls_on_their_own_stream(cuda_lib):
         for r in runs:
             assert all(torch.equal(a, b) for a, b in zip(r, e))
     cuda_lib.check()
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_monarch_call_right_behind_a_dense_one(cuda_lib, split):
+    """The Monarch kernels, which may start while the kernel before them
+    ends, read what an exact forward pass or decode has just written."""
+    B, H, b1, b2, d = 1, 4, 16, 20, 64
+    n = b1 * b2
+    q, k, v, _, _ = dense_case(B, H, H, n, 2600 if split else n, d, False, None, "head", BF16)
+    outs = []
+    for wait in (True, False, False):
+        o, _ = cuda_lib.monarch_attn_dense_fwd(q, k, v)
+        if wait:
+            torch.cuda.synchronize()
+        m = cuda_lib.monarch_attn_fwd(o, o, o, b1, b2, 1)
+        if wait:
+            torch.cuda.synchronize()
+        outs.append(cuda_lib.monarch_attn_dense_fwd(m, k, v)[0])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    cuda_lib.check()
