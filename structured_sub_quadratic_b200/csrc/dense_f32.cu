@@ -257,6 +257,18 @@ __device__ __forceinline__ void add_rows(float* rows, float (&acc)[N][4]) {
     }
 }
 
+// The sums of the warps that share 16 rows, in order, in the first of them.
+template <int WAYS, int DP, int N>
+__device__ __forceinline__ void join_ways(int way, float* rows, float (&acc)[N][4]) {
+#pragma unroll 1
+  for (int w = 1; w < WAYS; ++w) {
+    if (way == w) put_rows<DP>(rows, acc);
+    __syncthreads();
+    if (way == 0) add_rows<DP>(rows, acc);
+    __syncthreads();
+  }
+}
+
 // Keys past the length may hold anything: load_tile puts zeros in their
 // place, and their scores are masked by selection.
 
@@ -436,16 +448,16 @@ __global__ void __launch_bounds__(kDeltaThreads)
 // dK and dV of a tile of keys: every query head of the group and every query
 // tile that sees the keys, in order.
 //   P = exp(S - lse), dV = P^T dO, dS = P (dO V^T - delta), dK = scale dS^T Q
-// Of 256 channels, whose two sums do not fit a warp's registers, the two warps
-// that share 16 keys take half each (CHANNELS), over all queries, instead of
-// half the queries.
-template <typename T, int DP, int ROWS, int COLS, bool CHANNELS>
-__global__ void __launch_bounds__(4 * ROWS)
+// WAYS warps share 16 keys and a tile's queries.  Of 256 channels, whose two
+// sums do not fit a warp's registers, two warps take half each (CHANNELS), over
+// all queries.
+template <typename T, int DP, int ROWS, int COLS, int WAYS, bool CHANNELS>
+__global__ void __launch_bounds__(2 * ROWS * WAYS)
     dense_dkv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                      const float* __restrict__ lse, const float* __restrict__ delta,
                      const T* __restrict__ dout, T* __restrict__ dk, T* __restrict__ dv,
                      DenseProblem pb, bool vec) {
-  constexpr int kThreads = 4 * ROWS, kHalf = CHANNELS ? COLS : COLS / 2, N = kHalf / 8;
+  constexpr int kThreads = 2 * ROWS * WAYS, kOwn = CHANNELS ? COLS : COLS / WAYS, N = kOwn / 8;
   constexpr int kPart = CHANNELS ? DP / 2 : DP;
   extern __shared__ __align__(16) float smf[];
   float* sK = smf;
@@ -455,8 +467,8 @@ __global__ void __launch_bounds__(4 * ROWS)
   __shared__ float row_l2[COLS], row_dl[COLS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // first row, column and channel
-  const int wr = warp / 2 * 16, wc = CHANNELS ? 0 : warp % 2 * kHalf;
-  const int part = CHANNELS ? warp % 2 * kPart : 0;
+  const int wr = warp / WAYS * 16, way = warp % WAYS, wc = CHANNELS ? 0 : way * kOwn;
+  const int part = CHANNELS ? way * kPart : 0;
   const int tiles = (pb.Nk + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int k0 = (int)(blockIdx.x % tiles) * ROWS, hk = bh % pb.Hkv, b = bh / pb.Hkv;
   const int len = dense_len(pb, b), group = pb.H / pb.Hkv;
@@ -487,8 +499,8 @@ __global__ void __launch_bounds__(4 * ROWS)
         }
         tiles_arrived();
         float s[N][4], dp[N][4];
-        scores<kHalf, DP>(sK + wr * (DP + 4), sQ + wc * (DP + 4), s);
-        scores<kHalf, DP>(sV + wr * (DP + 4), sG + wc * (DP + 4), dp);
+        scores<kOwn, DP>(sK + wr * (DP + 4), sQ + wc * (DP + 4), s);
+        scores<kOwn, DP>(sV + wr * (DP + 4), sG + wc * (DP + 4), dp);
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -500,21 +512,16 @@ __global__ void __launch_bounds__(4 * ROWS)
             s[n][x] = p;
             dp[n][x] = see ? p * (dp[n][x] - row_dl[c]) : 0.f;
           }
-        accumulate<kHalf, DP>(s, sG + wc * (DP + 4) + part, av);
-        accumulate<kHalf, DP>(dp, sQ + wc * (DP + 4) + part, ak);
+        accumulate<kOwn, DP>(s, sG + wc * (DP + 4) + part, av);
+        accumulate<kOwn, DP>(dp, sQ + wc * (DP + 4) + part, ak);
       }
     }
   }
   tiles_arrived();
-  if constexpr (!CHANNELS) {  // the second warp's half of the queries, over K and V
-    if (wc > 0) {
-      put_rows<DP>(sK + wr * (DP + 4), ak);
-      put_rows<DP>(sV + wr * (DP + 4), av);
-    }
-    __syncthreads();
-    if (wc > 0) return;
-    add_rows<DP>(sK + wr * (DP + 4), ak);
-    add_rows<DP>(sV + wr * (DP + 4), av);
+  if constexpr (!CHANNELS) {  // the other warps' queries, over K and V
+    join_ways<WAYS, DP>(way, sK + wr * (DP + 4), ak);
+    join_ways<WAYS, DP>(way, sV + wr * (DP + 4), av);
+    if (way > 0) return;
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -532,19 +539,20 @@ __global__ void __launch_bounds__(4 * ROWS)
 }
 
 // dQ of a tile of queries: dQ = scale dS K over the tiles of visible keys.
-template <typename T, int DP, int ROWS, int COLS>
-__global__ void __launch_bounds__(4 * ROWS)
+template <typename T, int DP, int ROWS, int COLS, int WAYS>
+__global__ void __launch_bounds__(2 * ROWS * WAYS)
     dense_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                     const float* __restrict__ lse, const float* __restrict__ delta,
                     const T* __restrict__ dout, T* __restrict__ dq, DenseProblem pb, bool vec) {
-  constexpr int kThreads = 4 * ROWS, kHalf = COLS / 2, N = kHalf / 8;
+  constexpr int kThreads = 2 * ROWS * WAYS, kOwn = COLS / WAYS, N = kOwn / 8;
   extern __shared__ __align__(16) float smf[];
   float* sQ = smf;
   float* sG = sQ + ROWS * (DP + 4);
   float* sK = sG + ROWS * (DP + 4);
   float* sV = sK + COLS * (DP + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wr = warp / 2 * 16, wc = warp % 2 * kHalf;  // first row and column
+  // first row and column
+  const int wr = warp / WAYS * 16, way = warp % WAYS, wc = way * kOwn;
   const int tiles = (pb.Nq + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int q0 = (int)(blockIdx.x % tiles) * ROWS, h = bh % pb.H, b = bh / pb.H;
   const int hk = h / (pb.H / pb.Hkv);
@@ -575,8 +583,8 @@ __global__ void __launch_bounds__(4 * ROWS)
     load_tile<T, COLS, DP, kThreads>(sV, vb, pb.v.n, k0, len, pb.d, vec);
     tiles_arrived();
     float s[N][4], dp[N][4];
-    scores<kHalf, DP>(sQ + wr * (DP + 4), sK + wc * (DP + 4), s);
-    scores<kHalf, DP>(sG + wr * (DP + 4), sV + wc * (DP + 4), dp);
+    scores<kOwn, DP>(sQ + wr * (DP + 4), sK + wc * (DP + 4), s);
+    scores<kOwn, DP>(sG + wr * (DP + 4), sV + wc * (DP + 4), dp);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -585,14 +593,11 @@ __global__ void __launch_bounds__(4 * ROWS)
         const float p = exp2f(fmaf(s[n][x], sl, -l2[x >> 1]));
         s[n][x] = see ? p * (dp[n][x] - dl[x >> 1]) : 0.f;
       }
-    accumulate<kHalf, DP>(s, sK + wc * (DP + 4), acc);
+    accumulate<kOwn, DP>(s, sK + wc * (DP + 4), acc);
   }
   tiles_arrived();
-  // the second warp's half of the keys, over the queries
-  if (wc > 0) put_rows<DP>(sQ + wr * (DP + 4), acc);
-  __syncthreads();
-  if (wc > 0) return;
-  add_rows<DP>(sQ + wr * (DP + 4), acc);
+  join_ways<WAYS, DP>(way, sQ + wr * (DP + 4), acc);  // over the queries
+  if (way > 0) return;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int row = q0 + wr + lane / 4 + 8 * i;
@@ -650,54 +655,62 @@ cudaError_t forward_dp(const T* q, const T* k, const T* v, T* out, float* lse,
              : forward_rows<T, DP, 64>(q, k, v, out, lse, pb, split, vec, stream, launches);
 }
 
-template <typename T, int DP, int ROWS, int COLS>
+template <typename T, int DP, int ROWS, int COLS, int WAYS>
 cudaError_t dkv_rows(const T* q, const T* k, const T* v, const float* lse, const float* delta,
                      const T* dout, T* dk, T* dv, const DenseProblem& pb, bool vec,
                      cudaStream_t stream, int* launches) {
-  constexpr int smem =
-      2 * (ROWS + COLS) * (DP + 4) * (int)sizeof(float);
-  constexpr auto kernel = dense_dkv_kernel<T, DP, ROWS, COLS, (DP == 256)>;
+  constexpr int smem = 2 * (ROWS + COLS) * (DP + 4) * (int)sizeof(float);
+  constexpr auto kernel = dense_dkv_kernel<T, DP, ROWS, COLS, WAYS, (DP == 256)>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((pb.Nk + ROWS - 1) / ROWS) * pb.Hkv * pb.B;
   return timed_launch("dense_dkv_f32", stream, launches, [&] {
-    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, lse, delta, dout, dk, dv, pb, vec);
+    kernel<<<grid, 2 * ROWS * WAYS, smem, stream>>>(q, k, v, lse, delta, dout, dk, dv, pb, vec);
   });
 }
 
-template <typename T, int DP, int ROWS, int COLS>
+template <typename T, int DP, int ROWS, int COLS, int WAYS>
 cudaError_t dq_rows(const T* q, const T* k, const T* v, const float* lse, const float* delta,
                     const T* dout, T* dq, const DenseProblem& pb, bool vec, cudaStream_t stream,
                     int* launches) {
-  constexpr int smem =
-      2 * (ROWS + COLS) * (DP + 4) * (int)sizeof(float);
-  constexpr auto kernel = dense_dq_kernel<T, DP, ROWS, COLS>;
+  constexpr int smem = 2 * (ROWS + COLS) * (DP + 4) * (int)sizeof(float);
+  constexpr auto kernel = dense_dq_kernel<T, DP, ROWS, COLS, WAYS>;
   cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((pb.Nq + ROWS - 1) / ROWS) * pb.H * pb.B;
   return timed_launch("dense_dq_f32", stream, launches, [&] {
-    kernel<<<grid, 4 * ROWS, smem, stream>>>(q, k, v, lse, delta, dout, dq, pb, vec);
+    kernel<<<grid, 2 * ROWS * WAYS, smem, stream>>>(q, k, v, lse, delta, dout, dq, pb, vec);
   });
 }
 
-// TALL: rows of a CTA where there are many.
-template <typename T, int DP, int TALL, int COLS>
+// Fewer than one and a half CTAs of 32 rows per SM: four warps a row block.
+inline bool scarce(long rows, long heads) {
+  return 2 * ((rows + 31) / 32 * heads) < 3L * num_sms();
+}
+
+template <typename T, int DP>
 cudaError_t backward_dp(const T* q, const T* k, const T* v, const float* lse, const float* delta,
                         const T* dout, T* dq, T* dk, T* dv, const DenseProblem& pb, bool vec,
                         cudaStream_t stream, int* launches) {
-  constexpr int kSmall = DP == 64 ? COLS : 32;  // (registers of the two accumulators)
+  // (registers of the two sums of 128 channels; four tiles of 64 rows of 256
+  // channels exceed shared memory)
+  constexpr int kKeyCols = DP == 64 ? 64 : 32, kCols = DP == 256 ? 32 : 64;
+  constexpr int kTall = DP == 256 ? 32 : 64, kMany = DP == 256 ? 2 : 4;
   cudaError_t e = cudaSuccess;
-  if (pb.Nk > 0)
-    e = few(pb.Nk, (long)pb.Hkv * pb.B)
-            ? dkv_rows<T, DP, 32, kSmall>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
-                                        launches)
-            : dkv_rows<T, DP, TALL, kSmall>(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream,
-                                          launches);
-  if (e == cudaSuccess && pb.Nq > 0)
-    e = few(pb.Nq, (long)pb.H * pb.B)
-            ? dq_rows<T, DP, 32, COLS>(q, k, v, lse, delta, dout, dq, pb, vec, stream, launches)
-            : dq_rows<T, DP, TALL, COLS>(q, k, v, lse, delta, dout, dq, pb, vec, stream,
-                                         launches);
+  if (pb.Nk > 0) {
+    const long heads = (long)pb.Hkv * pb.B;
+    const auto run = scarce(pb.Nk, heads) ? dkv_rows<T, DP, 32, kCols, kMany>
+                     : few(pb.Nk, heads)  ? dkv_rows<T, DP, 32, kKeyCols, 2>
+                                          : dkv_rows<T, DP, kTall, kKeyCols, 2>;
+    e = run(q, k, v, lse, delta, dout, dk, dv, pb, vec, stream, launches);
+  }
+  if (e == cudaSuccess && pb.Nq > 0) {
+    const long heads = (long)pb.H * pb.B;
+    const auto run = scarce(pb.Nq, heads) ? dq_rows<T, DP, 32, kCols, kMany>
+                     : few(pb.Nq, heads)  ? dq_rows<T, DP, 32, kCols, 2>
+                                          : dq_rows<T, DP, kTall, kCols, 2>;
+    e = run(q, k, v, lse, delta, dout, dq, pb, vec, stream, launches);
+  }
   return e;
 }
 
@@ -761,15 +774,10 @@ cudaError_t dense_f32_backward(const T* q, const T* k, const T* v, const T* out,
   for (int x = 0; x < 7; ++x) vec = vec && rows_allow_four(p[x], s[x], sizeof(T));
   cudaError_t e = dense_delta<T>(out, dout, delta, pb, stream, launches);
   if (e != cudaSuccess) return e;
-  if (pb.d <= 64)
-    return backward_dp<T, 64, 64, 64>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
-                                  launches);
-  if (pb.d <= 128)
-    return backward_dp<T, 128, 64, 64>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
-                                   launches);
-  // four 64-row tiles of 256 channels exceed shared memory
-  return backward_dp<T, 256, 32, 32>(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream,
-                                 launches);
+  const auto backward = pb.d <= 64    ? backward_dp<T, 64>
+                        : pb.d <= 128 ? backward_dp<T, 128>
+                                      : backward_dp<T, 256>;
+  return backward(q, k, v, lse, delta, dout, dq, dk, dv, pb, vec, stream, launches);
 }
 
 template cudaError_t dense_f32_forward<float>(const float*, const float*, const float*, float*, float*,

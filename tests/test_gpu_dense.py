@@ -65,6 +65,8 @@ CASES = [
     (1, 1, 1, 40, 33, 256, True, None, "head"),
     (1, 2, 2, 70, 100, 64, True, None, "odd"),              # unaligned rows
     (2, 2, 1, 520, 520, 64, True, [520, 391], "head"),      # several tiles of either axis
+    (1, 40, 8, 40, 330, 64, True, [300], "token"),          # many short heads
+    (1, 60, 60, 300, 260, 16, False, None, "head"),
     # few queries over many keys: split over the keys and joined
     (1, 1, 1, 1, 2000, 64, False, None, "head"),
     (2, 2, 1, 70, 2500, 128, True, [2500, 700], "token"),   # ranges that one batch never reaches
