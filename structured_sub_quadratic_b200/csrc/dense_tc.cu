@@ -518,6 +518,10 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
 // tile of queries and walks the keys (dQ: three).  In both, eight warps hold
 // the score tile with two threads per TMEM lane (64 columns each: warps 0-3
 // the first, 4-7 the second half), warp 8 issues TMA and warp 9 the products.
+// P and dS are rounded to bf16 as operands, half a step each like the results;
+// every sum is fp32.  Bound: the products and the chain score, exponential,
+// product between them; 12 heads of 4680 x 128: dK and dV 243 us (1.11
+// PFLOP/s of their products), dQ 175 us (1.15).
 // ---------------------------------------------------------------------------
 struct BwdArgs {
   const float* lse;
