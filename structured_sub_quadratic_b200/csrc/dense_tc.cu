@@ -49,7 +49,8 @@ __device__ __forceinline__ uint4* row_unit(uint8_t* tile, int r, int u) {
 // (degree 5, by Remez exchange: 7e-8, 2e-7 in fp32, as the unit's), n added to
 // the exponent.  Hidden keys, at -inf, give 2^-149, which bf16 rounds to 0 and
 // a sum does not feel; what lies between 2^-127 and 2^-126 is only known to be
-// below 2^-126.
+// below 2^-126.  A NaN is lost here (at the clamp, and the exponent's sum would
+// turn one into a number): the row's maximum and other exponentials keep it.
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -127.f);
   x.y = fmaxf(x.y, -127.f);
@@ -162,7 +163,8 @@ __device__ __forceinline__ void accumulator_row(uint8_t* tile, int r, uint32_t t
 // x 128 scores at d = 128, against 2070 of products).  O stays in TMEM
 // under a running maximum that only moves when it grows by more than 2^8
 // (probabilities then reach 256, exact in the exponents of P's bf16 and of the
-// fp32 sum), so rescaling O is rare.  P overwrites S, rounded to bf16 as the
+// fp32 sum), so rescaling O is rare.  A score of NaN or +inf makes the maximum
+// NaN, and with it the row's exponentials, sum and result.  P overwrites S, rounded to bf16 as the
 // result is, and is the A operand of P V.  Bound: the exponential unit and
 // the FMA pipe at d = 64 (800 TFLOP/s), the products at d = 128, 12 heads of
 // 4680 in 137 us (0.98 PFLOP/s).
@@ -412,14 +414,15 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = fmaxf(s[16 * c], s[16 * c + 1]);
+        mx[c] = max3_nan(c ? s[16 * c] : m, s[16 * c], s[16 * c + 1]);
 #pragma unroll
-        for (int e = 2; e < 16; e += 2) mx[c] = max3(mx[c], s[16 * c + e], s[16 * c + e + 1]);
+        for (int e = 2; e < 16; e += 2) mx[c] = max3_nan(mx[c], s[16 * c + e], s[16 * c + e + 1]);
       }
-      const float mn = max3(max3(m, mx[0], mx[1]), mx[2], mx[3]);
+      float mn = max3_nan(mx[0], mx[1], max3_nan(mx[2], mx[3], mx[3]));
+      if (mn == INFINITY) mn = NAN;
       if (u == 0) {
         m = mn;
-      } else if (__any_sync(0xffffffffu, (mn - m) * sl > 8.f)) {
+      } else if (__any_sync(0xffffffffu, m != mn && !((mn - m) * sl <= 8.f))) {
         // O as step u - 1 leaves it: its P V is behind the other buffer's next phase
         if (!(ok = mbar_wait(s_full + 2 * t + (~u & 1), ((u + 1) >> 1) & 1, abort_flag, a.status)))
           break;
