@@ -262,9 +262,10 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
  * head h reads head h / (H / Hkv)); strides: q, k, v, out.  Key j is visible
  * to query i of batch b when j < k_lens[b] (device, B ints, or NULL; values
  * outside [0, Nk] count as the nearer end) and, if causal, j <= i + Nk - Nq.
- * A row without a visible key gets out = 0 and lse = -inf.  Keys past the
- * length may hold anything (NaN included); keys hidden by `causal` alone must
- * be finite.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
+ * A row without a visible key, or whose visible keys all score -inf, gets
+ * out = 0 and lse = -inf.  Keys past the length may hold anything (NaN
+ * included); keys hidden by `causal` alone must be finite.  A visible score of
+ * NaN or +inf makes its row NaN.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
  * for the product with v, sums are fp32.  fp32: operands are split into two
  * TF32 values and a product is off by 2^-20 of it at most; an infinity among
  * the visible values gives NaN.  scale > 0.  Few queries over many
@@ -301,7 +302,8 @@ MONARCH_API size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq);
  * sequence b is row j % page_size of page page_table[b][j / page_size]
  * (device, (B, max_pages) contiguous; entries past the sequence's pages are
  * not read).  lens: device, B ints, the keys of each sequence, 0 to
- * max_pages * page_size; a sequence of length 0 gets out = 0, lse = -inf.
+ * max_pages * page_size; a sequence of length 0, and a head whose keys all score
+ * -inf, gets out = 0, lse = -inf; a score of NaN or +inf makes the head's NaN.
  * lse: (B, H).  strides: q (batch, head, unused), k_cache and v_cache (page,
  * head, row), out (batch, head, unused).  Rows of a page past the length may
  * hold anything.  The cache is split over its length and joined in order.  A

@@ -350,7 +350,8 @@ def monarch_attn_dense_fwd(q, k, v, causal=False, k_lens=None, scale=None, out=N
 
     ``causal``: query i sees the keys up to i + Nk - Nq.  ``k_lens``: int32
     (B,) on the device, the keys of each sequence that count; what lies past
-    them is never used.  A row that sees no key gets out = 0, lse = -inf.
+    them is never used.  A row that sees no key (or only keys that score -inf)
+    gets out = 0, lse = -inf.
     ``scale`` defaults to 1/sqrt(d).  lse is fp32 (B, H, Nq), for
     ``monarch_attn_dense_bwd``.
     """

@@ -119,8 +119,8 @@ __device__ __forceinline__ void join_warps(const float (*m)[kRows], const float 
       zz = fmaf(z[w][h], f, zz);
       acc = fmaf(o[w * o_step + h * pitch + e], f, acc);
     }
-    if (sp.chunks == 1) {
-      out[s.b * pb.out_b + (s.h0 + h) * pb.out_h + e] = from_f32<T>(acc / zz);
+    if (sp.chunks == 1) {  // (zz 0: every key scores -inf, as if there were none)
+      out[s.b * pb.out_b + (s.h0 + h) * pb.out_h + e] = from_f32<T>(zz == 0.f ? 0.f : acc / zz);
       if (e == 0) lse[row0 + h] = (mm + log2f(zz)) * kLn2;
     } else {
       const long at = (long)s.c * pb.B * pb.H + row0 + h;
@@ -603,9 +603,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     float a = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) a += sa[w][tid];
-    out[b * pb.out_b + h * pb.out_h + tid] = from_f32<T>(n > 0 ? a / zz : 0.f);
+    out[b * pb.out_b + h * pb.out_h + tid] = from_f32<T>(zz == 0.f ? 0.f : a / zz);
   }
-  if (tid == 0) lse[row] = n > 0 ? (m + log2f(zz)) * kLn2 : -INFINITY;
+  if (tid == 0) lse[row] = (m + log2f(zz)) * kLn2;  // (-inf without keys)
 }
 
 bool rows_allow(const void* p, std::initializer_list<long> strides, long elements, size_t elt) {

@@ -6,11 +6,12 @@
 //   lse = log of the sum of exp(S) over them.
 // Key j is visible to query i of batch b when j < k_lens[b] and, for causal
 // calls, j <= i + Nk - Nq (the last query sees every key).  A row without a
-// visible key has O = 0, lse = -inf and no gradient.  Query head h reads
-// key/value head h / (H / Hkv).
+// visible key, or whose visible keys all score -inf, has O = 0, lse = -inf and
+// no gradient.  Query head h reads key/value head h / (H / Hkv).
 #pragma once
 
 #include <limits.h>
+#include <math.h>
 
 #include "common.cuh"
 
@@ -38,6 +39,11 @@ __device__ __forceinline__ int dense_len(const DenseProblem& pb, int b) {
 // Keys [0, n) visible to query i of a batch with `len` keys.
 __device__ __forceinline__ int dense_visible(const DenseProblem& pb, int len, int i) {
   return pb.causal ? max(0, min(len, i + pb.Nk - pb.Nq + 1)) : len;
+}
+
+// A row's lse in log2 units, for P = exp2(S - lse): P = 0 in a row without weights.
+__device__ __forceinline__ float dense_lse2(float lse) {
+  return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
 }
 
 // A forward pass of few CTAs cuts the keys into `splits` ranges of `per` key

@@ -372,10 +372,10 @@ __global__ void __launch_bounds__(4 * ROWS)
   for (int i = 0; i < 2; ++i) {
     const int row = q0 + wr + lane / 4 + 8 * i;
     if (row >= pb.Nq) continue;
-    const bool any = vis[i] > first;
     const float m1 = other_m[row - q0], mn = fmaxf(m[i], m1), base = mn == -INFINITY ? 0.f : mn;
     const float f0 = exp2f(m[i] - base), f1 = exp2f(m1 - base);
     const float sum = z[i] * f0 + other_z[row - q0] * f1;
+    const bool any = sum != 0.f;  // a visible key, not all of them at -inf
     const bool whole = split.splits == 1;
     const float inv = whole ? 1.f / sum : 1.f;
     const long at = (((long)range * pb.B + b) * pb.H + h) * pb.Nq + row;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(2 * ROWS * WAYS)
         for (int x = threadIdx.x; x < COLS; x += kThreads) {
           // a row outside the tensor or without keys: exp(S - inf) = 0
           const bool live = q0 + x < pb.Nq && dense_visible(pb, len, q0 + x) > 0;
-          row_l2[x] = live ? __ldg(lse + row0 + q0 + x) * kLog2e : INFINITY;
+          row_l2[x] = live ? dense_lse2(__ldg(lse + row0 + q0 + x)) : INFINITY;
           row_dl[x] = live ? __ldg(delta + row0 + q0 + x) : 0.f;
         }
         tiles_arrived();
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(2 * ROWS * WAYS)
     const bool ok = row < pb.Nq;
     const long at = ((long)b * pb.H + h) * pb.Nq + row;
     vis[i] = ok ? dense_visible(pb, len, row) : 0;
-    l2[i] = ok ? __ldg(lse + at) * kLog2e : 0.f;
+    l2[i] = ok ? dense_lse2(__ldg(lse + at)) : 0.f;
     dl[i] = ok ? __ldg(delta + at) : 0.f;
   }
   const int end = dense_visible(pb, len, min(q0 + ROWS, pb.Nq) - 1);

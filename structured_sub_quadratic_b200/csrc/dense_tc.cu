@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
       if (ok && nj > 0)  // P V of the last step
         ok = mbar_wait(s_full + 2 * t + (~nj & 1), ((nj + 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
-      const bool any = vis > 0;
+      const bool any = m != -INFINITY;  // a visible key, not all of them at -inf
       if (ok && a.split.splits > 1) {
         if (row < pb.Nq) {
           const long at = (((long)split * pb.B + b) * pb.H + h) * pb.Nq + row;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // a row outside the tensor or without keys: exp(S - inf) = 0
         const int row = q0 + x * 32 + lane;
         const bool live = row < pb.Nq && dense_visible(pb, len, row) > 0;
-        l2[x] = live ? __ldg(a.lse + at + row) * kLog2e : INFINITY;
+        l2[x] = live ? dense_lse2(__ldg(a.lse + at + row)) : INFINITY;
         dl[x] = live ? __ldg(a.delta + at + row) : 0.f;
       }
       if (i >= 2 && !warp_wait(g_empty + st, par, abort_flag, a.status)) break;
@@ -780,13 +780,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         p[e + 2] = ex2(w.x);
         p[e + 3] = ex2(w.y);
       }
-      // the first column whose query sees this key
+      // the first column whose query sees this key, and the end of the queries:
+      // the zeros behind them times an infinite key are NaN (two selections; one
+      // over both ends slows every tile, 12 heads of 4680 238 -> 269 us)
       const int lo = (key >= len ? kTile : pb.causal ? key - shift - q0 : 0) - half * 64;
+      const int hi = pb.Nq - q0 - half * 64;
       const bool masked = k0 + kTile > len || (pb.causal && k0 + kTile - 1 > q0 + shift);
       if (masked) {
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e < lo) p[e] = 0.f;
+      }
+      if (hi < 64) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= hi) p[e] = 0.f;
       }
       store_half(ts, p);
       tmem_wait_st();
@@ -807,6 +815,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e < lo) d[e] = 0.f;
+      }
+      if (hi < 64) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= hi) d[e] = 0.f;
       }
       store_half(tp, d);
       tmem_wait_st();
@@ -1004,7 +1017,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int vis = dense_visible(pb, len, row), all = dense_visible(pb, len, q0);
     const long at = ((long)b * pb.H + h) * pb.Nq + row;
     const bool live = row < pb.Nq && vis > 0;
-    const float lse2 = live ? __ldg(a.lse + at) * kLog2e : INFINITY;
+    const float lse2 = live ? dense_lse2(__ldg(a.lse + at)) : INFINITY;
     const float delta = !DELTA && live ? __ldg(a.delta + at) : 0.f;
     float sum = 0.f;
     const float sl = pb.scale * kLog2e;

@@ -1,8 +1,9 @@
-"""Exact attention where values are not numbers."""
+"""Exact attention where values are not numbers or scores are infinite."""
 import pytest
 import torch
 
-from test_gpu_dense import BF16, F32, decode_case, dense_case
+from oracle import dense_ref
+from test_gpu_dense import BF16, F32, close, decode_case, dense_case, f64, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,61 @@ def test_no_cached_key_hides_a_nan(cuda_lib, keys, H, Hkv, dtype):
     last = H - H // Hkv
     assert torch.isnan(out[:, :last]).all() and torch.isnan(lse[:, :last]).all()
     assert torch.equal(out[:, last:], clean[:, last:])
+
+
+# --------------------------------------------------------------------------
+# scores of -inf
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 24, 128])
+@pytest.mark.parametrize("Nq,Nk", [(70, 150), (200, 600), (2, 2600)])
+def test_scores_of_minus_infinity(cuda_lib, Nq, Nk, d):
+    """Keys that score -inf weigh nothing; a row that has no others is a row
+    without keys, in one range of keys or several, and takes no part in the
+    gradients."""
+    q, k, v, do, _ = dense_case(1, 3, 3, Nq, Nk, d, False, None, "head", BF16)
+    q[..., 0] = q[..., 0].abs() + 1
+    k[0, 0, :, 0] = -INF                     # every key of head 0
+    gone = torch.arange(Nk, device="cuda") % 7 < 3
+    k[0, 1, gone, 0] = -INF                  # some keys of head 1
+    out, lse = cuda_lib.monarch_attn_dense_fwd(q, k, v)
+    _, dk, dv = cuda_lib.monarch_attn_dense_bwd(q, k, v, out, lse, do)
+    cuda_lib.check()
+    assert (out[0, 0] == 0).all() and torch.isneginf(lse[0, 0]).all()
+    assert (dk[0, 0] == 0).all() and (dv[0, 0] == 0).all()
+    for h, kept in ((1, ~gone), (2, torch.ones_like(gone))):
+        x = [f64(t) for t in (q[:, h:h + 1], k[:, h:h + 1, kept], v[:, h:h + 1, kept],
+                              do[:, h:h + 1])]
+        refs = (*dense_ref.dense_forward(*x[:3]), *dense_ref.dense_backward(*x)[1:])
+        eO, eL, _, eK, eV = dense_ref.dense_errors(*x, half_step(BF16))
+        got = (out[:, h:h + 1], lse[:, h:h + 1], dk[:, h:h + 1, kept], dv[:, h:h + 1, kept])
+        # (a sum of all keys for one of the kept ones: 7 / 4 of its terms)
+        for name, a, ref, e in zip(("out", "lse", "dk", "dv"), got, refs, (eO, eL, eK, eV)):
+            close(name, a, ref, 1.75 * e)
+
+
+@pytest.mark.parametrize("Nq,Nk", [(40, 100), (2, 2000)])
+def test_scores_that_overflow(cuda_lib, Nq, Nk):
+    """fp32 scores of -1e40 are -inf: rows without keys, split or not."""
+    q, v, do = (torch.full((1, 2, n, 32), x, device="cuda")
+                for n, x in ((Nq, 1e20), (Nk, 1.0), (Nq, 1.0)))
+    k = torch.full_like(v, -1e20)
+    out, lse = cuda_lib.monarch_attn_dense_fwd(q, k, v)
+    grads = cuda_lib.monarch_attn_dense_bwd(q, k, v, out, lse, do)
+    cuda_lib.check()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert all((g == 0).all() for g in grads)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (40, 2)])
+@pytest.mark.parametrize("keys", [100, 3000])
+def test_cached_scores_of_minus_infinity(cuda_lib, keys, H, Hkv, dtype):
+    q, k, v, table, lens = decode_case(1, H, Hkv, [keys], 16, 64, dtype)
+    q[..., 0] = q[..., 0].abs() + 1
+    clean, _ = cuda_lib.monarch_attn_dense_decode(q, k, v, table, lens)
+    k[:, 0, :, 0] = -INF
+    out, lse = cuda_lib.monarch_attn_dense_decode(q, k, v, table, lens)
+    cuda_lib.check()
+    first = H // Hkv
+    assert (out[:, :first] == 0).all() and torch.isneginf(lse[:, :first]).all()
+    assert torch.equal(out[:, first:], clean[:, first:])
