@@ -6,6 +6,8 @@
 
 #include <math.h>
 
+#include <initializer_list>
+
 #include "dense.cuh"
 #include "entry.cuh"
 
@@ -63,6 +65,18 @@ bool distinct(const View& v) {
 bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
   const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
   return na && nb && x < y + nb && y < x + na;
+}
+
+// The lengths of a dense call: aligned, and apart from what it writes.
+bool lens_ok(const int* k_lens, int B, std::initializer_list<View> outputs, size_t elt,
+             const void* lse, size_t lse_bytes, const void* workspace, size_t workspace_bytes) {
+  if (!k_lens) return true;
+  if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return false;
+  const size_t n = B * sizeof(int);
+  for (const View& o : outputs)
+    if (!o.empty() && ranges_meet(o.ptr, o.extent() * elt, k_lens, n)) return false;
+  return !ranges_meet(lse, lse_bytes, k_lens, n) &&
+         !ranges_meet(workspace, workspace_bytes, k_lens, n);
 }
 
 bool views_meet(const View& a, const View& b, size_t elt) {
@@ -169,7 +183,8 @@ int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* 
                  ranges_meet(out, o.extent() * elt, lse, lse_bytes) ||
                  ranges_meet(out, o.extent() * elt, workspace, need)))
     return MONARCH_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return MONARCH_ERR_INVALID_ARG;
+  if (!lens_ok(k_lens, B, {o}, elt, lse, lse_bytes, workspace, need))
+    return MONARCH_ERR_INVALID_ARG;
   cudaError_t e;
   if (dtype == MONARCH_DTYPE_F32) {
     e = monarch::dense_f32_forward<float>(
@@ -239,7 +254,8 @@ int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* 
                           ranges_meet(lse, lse_bytes, o[a].ptr, o[a].extent() * elt)))
       return MONARCH_ERR_INVALID_ARG;
   }
-  if (reinterpret_cast<uintptr_t>(k_lens) % sizeof(int)) return MONARCH_ERR_INVALID_ARG;
+  if (!lens_ok(k_lens, B, {o[0], o[1], o[2]}, elt, nullptr, 0, workspace, need))
+    return MONARCH_ERR_INVALID_ARG;
   float* delta = static_cast<float*>(workspace);
   cudaError_t e;
   if (dtype == MONARCH_DTYPE_F32) {

@@ -1,0 +1,32 @@
+"""Refusals of the exact-attention entry points that concern arguments beside
+q, k and v (fake pointers, as no device call is made).  CPU only."""
+import pytest
+
+from structured_sub_quadratic_b200 import _build, api
+
+P = 1 << 30  # fake pointers, 1 GiB apart
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return api.load_library()
+
+
+@pytest.mark.parametrize("sizes,lens", [
+    ((2, 4, 2, 16, 16, 64), 4 * P + 64),            # out
+    ((2, 4, 2, 16, 16, 64), 5 * P + 4),             # lse
+    ((2, 4, 2, 16, 16, 64), 5 * P + 2 * 4 * 16 * 4 - 4),  # its last element
+    ((2, 4, 2, 16, 16, 64), 5 * P - 4),             # the second length in its first one
+    ((1, 4, 2, 1, 4096, 64), 10 * P + 128),         # the workspace of a split call
+])
+def test_forward_refuses_outputs_over_the_lengths(lib, sizes, lens):
+    assert lib.monarch_attn_dense_fwd(0, P, 2 * P, 3 * P, 4 * P, 5 * P, *sizes, None, 0, lens,
+                                      0.125, 10 * P, 1 << 24, None) == api.MONARCH_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("lens", [7 * P + 4, 8 * P, 9 * P + 8, 10 * P + 4, 7 * P - 4])
+def test_backward_refuses_outputs_over_the_lengths(lib, lens):
+    ptrs = [(i + 1) * P for i in range(9)]  # ..., dq, dk, dv
+    assert lib.monarch_attn_dense_bwd(0, *ptrs, 2, 4, 2, 16, 16, 64, None, 0, lens, 0.125, 10 * P,
+                                      1 << 20, None) == api.MONARCH_ERR_INVALID_ARG
