@@ -307,9 +307,9 @@ MONARCH_API size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq);
  * lse: (B, H).  strides: q (batch, head, unused), k_cache and v_cache (page,
  * head, row), out (batch, head, unused).  Rows of a page past the length may
  * hold anything.  The cache is split over its length and joined in order.  A
- * page index outside [0, n_pages) contributes a zero key and value, a length
- * outside its range counts as the nearer end, and monarch_attn_check then
- * reports MONARCH_ERR_BAD_INDEX.  workspace: device, 16-byte aligned,
+ * page index outside [0, n_pages) stands for zero keys and values (which score
+ * 0 and keep their weight in the softmax), a length outside its range counts as
+ * the nearer end, and monarch_attn_check then reports MONARCH_ERR_BAD_INDEX.  workspace: device, 16-byte aligned,
  * monarch_attn_dense_decode_workspace_bytes. */
 MONARCH_API int monarch_attn_dense_decode(int dtype, const void* q, const void* k_cache,
                                           const void* v_cache, const int* page_table,

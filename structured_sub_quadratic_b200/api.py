@@ -415,8 +415,9 @@ def monarch_attn_dense_decode(q, k_cache, v_cache, page_table, lens, scale=None,
     transpose(1, 2)).  page_table: int32 (B, max_pages); key j of sequence b is
     row j % page_size of page page_table[b, j // page_size].  lens: int32
     (B,), the keys of each sequence (0: out = 0, lse = -inf).  lse is fp32
-    (B, H).  Pages and lengths are checked on the device: ``check`` raises
-    MONARCH_ERR_BAD_INDEX after one that lay outside the cache.
+    (B, H).  Pages and lengths are checked on the device: one that lies outside
+    the cache stands for zero keys and values, or counts as the nearer end, and
+    ``check`` then raises MONARCH_ERR_BAD_INDEX.
     """
     lib = load_library()
     if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:

@@ -83,8 +83,8 @@ __device__ __forceinline__ Share share_of(const DecodeProblem& pb, const Split& 
   return s;
 }
 
-// Page and row of key j, page -1 where there is none or it lies outside the
-// cache (which is recorded).
+// Page and row of key j, page -1 where there is none (its score is masked) or it
+// lies outside the cache (which is recorded; the key and value are zeros).
 __device__ __forceinline__ int2 place(const DecodeProblem& pb, const Share& s, int j,
                                       int* status) {
   if (j >= s.j1) return make_int2(-1, 0);

@@ -726,8 +726,8 @@ const char* monarch_attn_strerror(int status) {
       return "the shape needs more scratch than the 64 MiB static array of "
              "monarch_attn_fwd_noalloc holds";
     case MONARCH_ERR_BAD_INDEX:
-      return "a page table entry or a sequence length lay outside the cache; its keys were left "
-             "out";
+      return "a page table entry lay outside the cache and its keys and values were taken as "
+             "zeros, or a sequence length did and the nearer end was taken";
     default: return "unknown status";
   }
 }

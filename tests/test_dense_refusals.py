@@ -30,3 +30,9 @@ def test_backward_refuses_outputs_over_the_lengths(lib, lens):
     ptrs = [(i + 1) * P for i in range(9)]  # ..., dq, dk, dv
     assert lib.monarch_attn_dense_bwd(0, *ptrs, 2, 4, 2, 16, 16, 64, None, 0, lens, 0.125, 10 * P,
                                       1 << 20, None) == api.MONARCH_ERR_INVALID_ARG
+
+
+def test_text_of_a_bad_index_says_what_the_kernels_do(lib):
+    """Keys of a page outside the cache are zeros, and stay in the softmax."""
+    text = lib.monarch_attn_strerror(api.MONARCH_ERR_BAD_INDEX)
+    assert b"zero" in text and b"left out" not in text

@@ -1,9 +1,11 @@
-"""Exact attention where values are not numbers or scores are infinite."""
+"""Exact attention where values are not numbers, scores are infinite or pages lie
+outside the cache."""
+import numpy as np
 import pytest
 import torch
 
 from oracle import dense_ref
-from test_gpu_dense import BF16, F32, close, decode_case, dense_case, f64, half_step
+from test_gpu_dense import BF16, F32, close, decode_bounds, decode_case, dense_case, f64, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +107,32 @@ def test_cached_scores_of_minus_infinity(cuda_lib, keys, H, Hkv, dtype):
     first = H // Hkv
     assert (out[:, :first] == 0).all() and torch.isneginf(lse[:, :first]).all()
     assert torch.equal(out[:, first:], clean[:, first:])
+
+
+# --------------------------------------------------------------------------
+# pages outside the cache
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keys,page", [(100, 16), (100, 7), (2500, 64)])
+def test_keys_of_bad_pages_are_zero(cuda_lib, keys, page, dtype):
+    """A page outside the cache stands for zero keys and values, which score 0."""
+    q, k, v, table, lens = decode_case(2, 4, 2, [keys, 20], page, 64, dtype, spare=3)
+    spare = torch.ones(k.shape[0], dtype=torch.bool, device="cuda")
+    spare[table.flatten().long()] = False
+    zero = int(spare.nonzero()[0])
+    k[zero], v[zero] = 0, 0
+    bad, ref = table.clone(), table.clone()
+    bad[0, 1], bad[0, 3] = -1, k.shape[0]
+    ref[0, 1], ref[0, 3] = zero, zero
+    out, lse = cuda_lib.monarch_attn_dense_decode(q, k, v, bad, lens)
+    with pytest.raises(cuda_lib.MonarchError) as exc:
+        cuda_lib.check()
+    assert exc.value.status == cuda_lib.MONARCH_ERR_BAD_INDEX
+    x = [f64(t) for t in (q, k, v)]
+    O, L, A = dense_ref.decode(*x, ref.cpu().numpy(), lens.tolist())
+    eO, eL = decode_bounds(*x, O, A, lens.tolist(), dtype)
+    close("out", out, O, eO)
+    close("lse", lse, L, np.full(L.shape, eL))
+    assert all(torch.equal(a, b) for a, b in zip(
+        (out, lse), cuda_lib.monarch_attn_dense_decode(q, k, v, ref, lens)))
+    cuda_lib.check()
