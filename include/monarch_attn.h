@@ -282,9 +282,11 @@ MONARCH_API size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int 
 
 /* Gradients of sum(out * dout) with respect to q, k and v; the probabilities
  * are recomputed from q, k and lse.  out and lse: what
- * monarch_attn_dense_fwd gave for the same arguments (over up to 512 keys the
- * tensor-core kernels take the row sums of dout out from the probabilities
- * instead of the rounded out).  strides: q, k, v, out,
+ * monarch_attn_dense_fwd gave for the same arguments (the tensor-core kernels
+ * take the row sums of dout out from the probabilities instead of the rounded
+ * out in tiles of 128 queries that see up to 512 keys; elsewhere dq and dk carry
+ * the rounding of out, relative to the values themselves, not to how they
+ * differ from key to key).  strides: q, k, v, out,
  * dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
  * does a query without a visible key.  workspace: device, 16-byte aligned,
  * monarch_attn_dense_bwd_workspace_bytes. */

@@ -77,7 +77,7 @@ def dense_backward(q, k, v, dout, causal=False, lens=None, scale=None):
 
 
 def dense_errors(q, k, v, dout, half_step, causal=False, lens=None, scale=None,
-                 rounded_weights=True):
+                 rounded_weights=True, exact_delta=False):
     """Bounds on |error| of (O, lse, dq, dk, dv), element by element.
 
     half_step: finfo(dtype).eps / 2 of the tensors, by which every output is
@@ -86,8 +86,9 @@ def dense_errors(q, k, v, dout, half_step, causal=False, lens=None, scale=None,
     is off by at most n eps32 times the sum of their magnitudes (eps32 = 2^-23
     covers truncating accumulators), and the exponential by 2^-21:
       p is off by e p,   e = 2 (d + 8) eps32 scale |q| |k|  + 2^-21 + Nk eps32
-    (the score's error, twice for that of the row's log-sum-exp); delta is
-    taken from the rounded O.
+    (the score's error, twice for that of the row's log-sum-exp).  delta is
+    taken from the rounded O, or, in the rows of exact_delta (one truth value, or
+    (B, 1, Nq)), from the unrounded P and dP.
     """
     B, H, Nq, d = q.shape
     Hkv, Nk = k.shape[1], k.shape[2]
@@ -107,6 +108,8 @@ def dense_errors(q, k, v, dout, half_step, causal=False, lens=None, scale=None,
     dS = P * (dP - (P * dP).sum(-1, keepdims=True))
     adP = np.abs(dout) @ np.abs(vv).swapaxes(-1, -2)
     eD = (np.abs(dout) * (eO + d * eps * np.abs(O))).sum(-1, keepdims=True)
+    eP = ((e + Nk * eps) * P * np.abs(dP) + d * eps * P * adP).sum(-1, keepdims=True)
+    eD = np.where(np.broadcast_to(exact_delta, (B, 1, Nq))[..., None], eP, eD)
     edS = (w + e) * np.abs(dS) + P * (d * eps * adP + eD)
 
     def gather(x):

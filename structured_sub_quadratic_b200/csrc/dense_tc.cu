@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
 
 // ---------------------------------------------------------------------------
 // Backward.  The probabilities are recomputed from q, k and lse; delta is the
-// row sum of dO O.  Two kernels, so that no sum needs atomics: one owns a tile
+// row sum of dO O, from one form of it or another (kExactTiles).  Two kernels, so that no sum needs atomics: one owns a tile
 // of keys and walks the queries (dK, dV: four products a tile), the other a
 // tile of queries and walks the keys (dQ: three).  In both, eight warps hold
 // the score tile with two threads per TMEM lane (64 columns each: warps 0-3
@@ -535,6 +535,17 @@ struct BwdArgs {
 };
 
 constexpr int kBwdThreads = 320;
+
+// delta = row sum of dO O = row sum of P (dO V^T).  O is rounded to bf16, and
+// where the values share a large part, which dO V^T - delta cancels, its
+// rounding is most of dQ and dK (values of 256 or 258: all of them); with few
+// keys it shows for any values (36 causal keys: error 2.8e-3 of dQ and dK
+// against 2.4e-3, of which the roundings of dS and of the result are the rest).
+// So tiles of queries that see up to 512 keys take the second form, whatever the
+// length of the tensors that their sequence shares, at the price of two more
+// products (five in dQ, for three) and a second walk over their keys; longer
+// tiles take the first.
+constexpr int kExactTiles = 4;
 
 // The 64 columns of a thread as bf16 pairs, over its own half of a score tile.
 __device__ __forceinline__ void store_half(uint32_t taddr, const float (&x)[64]) {
@@ -856,29 +867,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // dQ of 128 queries of a head: dQ = scale sum over the key tiles of dS K,
 // dS = P (dO V^T - delta).  P stays in registers, so the next S starts as soon
 // as this one is read, and runs beside its exponentials.
-// DELTA: the row sums of P (dO V^T) instead, into a.delta.
-template <int D, bool DELTA>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    dense_dq_tc_kernel(const __grid_constant__ TileMap mq, const __grid_constant__ TileMap mk,
-                       const __grid_constant__ TileMap mv, const __grid_constant__ TileMap mg,
-                       const __grid_constant__ TileMap mdq, const __grid_constant__ BwdArgs a) {
-  using L = BwdLayout<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  if (smem_u32(smem) & 1023u) {
-    if (tid == 0) atomicExch(a.status, 2);
-    return;
-  }
-  const DenseProblem& pb = a.pb;
-  const int heads = pb.B * pb.H;
-  const int tile = pb.causal ? a.tiles - 1 - blockIdx.x / heads : blockIdx.x % a.tiles;
-  const int bh = pb.causal ? blockIdx.x % heads : blockIdx.x / a.tiles;
-  const int h = bh % pb.H, b = bh / pb.H, hk = h / (pb.H / pb.Hkv);
-  const int q0 = tile * kTile;
-  const int len = dense_len(pb, b);
-  const int n = (dense_visible(pb, len, min(q0 + kTile, pb.Nq) - 1) + kTile - 1) / kTile;
-  const int tail = n * kTile > len && len < pb.Nk ? len - (n - 1) * kTile : kTile;
+// TWICE: a first walk over the same tiles sums delta from P (dO V^T) and leaves
+// it for dK and dV, too.
+struct DqTile {
+  int h, b, hk, q0, len, n, tail;  // n key tiles, the last with `tail` rows up to the length
+};
 
+template <int D, bool TWICE>
+__device__ __forceinline__ void dq_tile(uint8_t* smem, uint32_t tmem, const TileMap& mq,
+                                        const TileMap& mk, const TileMap& mv, const TileMap& mg,
+                                        const TileMap& mdq, const BwdArgs& a, const DqTile& x,
+                                        int warp) {
+  using L = BwdLayout<D>;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const DenseProblem& pb = a.pb;
+  const int n = x.n, q0 = x.q0, steps = TWICE ? 2 * n : n;
+  auto key_tile_of = [&](int j) { return TWICE && j >= n ? j - n : j; };
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* qg_full = bars;
   uint64_t* k_full = bars + 1;   // [stages]
@@ -891,33 +895,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* dp_full = bars + 12;
   uint64_t* ds_full = bars + 13;
   uint64_t* done = bars + 14;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 16);
-  if (tid == 0) {
-    mbar_init(qg_full, 1);
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(k_full + s, 1);
-      mbar_init(v_full + s, 1);
-      mbar_init(k_empty + s, 1);
-      mbar_init(v_empty + s, 1);
-    }
-    mbar_init(k_tail, 1);
-    mbar_init(s_full, 1);
-    mbar_init(s_read, 8);
-    mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
-    mbar_init(done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, L::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 8) {
     // ---- TMA: Q and dO, then K and V tile by tile ----
@@ -925,30 +903,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int kt = 0, vt = 0;
     if (lane == 0 && n > 0) {
       mbar_arrive_expect_tx(qg_full, 2 * L::kTileBytes);
-      load_tile<D>(smem + L::kAOff, mq, qg_full, q0, h, b);
-      load_tile<D>(smem + L::kBOff, mg, qg_full, q0, h, b);
-      for (int j = 0; j < n; ++j) {
-        const int st = j & 1;
+      load_tile<D>(smem + L::kAOff, mq, qg_full, q0, x.h, x.b);
+      load_tile<D>(smem + L::kBOff, mg, qg_full, q0, x.h, x.b);
+      for (int j = 0; j < steps; ++j) {
+        const int st = j & 1, row = key_tile_of(j) * kTile;
         const uint32_t par = ((j >> 1) - 1) & 1;
         if (j >= 2 && !(ok = mbar_wait(k_empty + st, par, abort_flag, a.status))) break;
         mbar_arrive_expect_tx(k_full + st, L::kTileBytes);
-        load_tile<D>(smem + L::kXOff + st * L::kTileBytes, mk, k_full + st, j * kTile, hk, b);
+        load_tile<D>(smem + L::kXOff + st * L::kTileBytes, mk, k_full + st, row, x.hk, x.b);
         kt = j + 1;
         if (j >= 2 && !(ok = mbar_wait(v_empty + st, par, abort_flag, a.status))) break;
         mbar_arrive_expect_tx(v_full + st, L::kTileBytes);
-        load_tile<D>(smem + L::kYOff + st * L::kTileBytes, mv, v_full + st, j * kTile, hk, b);
+        load_tile<D>(smem + L::kYOff + st * L::kTileBytes, mv, v_full + st, row, x.hk, x.b);
         vt = j + 1;
       }
     }
     __syncwarp();
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok && n > 0 && tail < kTile) {
+    if (ok && n > 0 && x.tail < kTile) {
       // keys past the length may hold anything (0 x NaN): zeros in their place
-      const int st = (n - 1) & 1;
-      if (mbar_wait(k_full + st, ((n - 1) >> 1) & 1, abort_flag, a.status)) {
+      // (a first walk selects their products away)
+      const int st = (steps - 1) & 1;
+      if (mbar_wait(k_full + st, ((steps - 1) >> 1) & 1, abort_flag, a.status)) {
         uint8_t* sk = smem + L::kXOff + st * L::kTileBytes;
-        for (int x = lane; x < (kTile - tail) * L::kCh * 8; x += 32)
-          *row_unit(sk, tail + x / (L::kCh * 8), x % (L::kCh * 8)) = make_uint4(0, 0, 0, 0);
+        for (int y = lane; y < (kTile - x.tail) * L::kCh * 8; y += 32)
+          *row_unit(sk, x.tail + y / (L::kCh * 8), y % (L::kCh * 8)) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_tail);
@@ -972,7 +951,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       constexpr uint64_t kStep = L::kTileBytes >> 4;
       auto key_tile = [&](int j) {
         return warp_wait(k_full + (j & 1), (j >> 1) & 1, abort_flag, a.status) &&
-               (j + 1 < n || tail == kTile || warp_wait(k_tail, 0, abort_flag, a.status));
+               (j + 1 < steps || x.tail == kTile || warp_wait(k_tail, 0, abort_flag, a.status));
       };
       bool ok = warp_wait(qg_full, 0, abort_flag, a.status) && key_tile(0);
       if (ok) {
@@ -986,9 +965,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         warp_commit(v_empty);
       }
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
+      for (int j = 0; j < steps && ok; ++j) {
         const int st = j & 1, s1 = st ^ 1;
-        const bool more = j + 1 < n;
+        const bool more = j + 1 < steps;
         if (more) {
           if (!(ok = key_tile(j + 1) && warp_wait(s_read, j & 1, abort_flag, a.status))) break;
           tc_fence_after();
@@ -998,7 +977,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!(ok = warp_wait(ds_full, j & 1, abort_flag, a.status))) break;
         tc_fence_after();
-        if (!DELTA) mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol, xm + st * kStep, j > 0);
+        if (!TWICE || j >= n)
+          mma_halves<D>(tmem + L::kAccCol, tmem + L::kDPCol, xm + st * kStep, key_tile_of(j) > 0);
         warp_commit(k_empty + st);
         if (more) {  // (in order: over dS once dQ has read it)
           mma_nt<D>(tmem + L::kDPCol, dg, yk + s1 * kStep);
@@ -1014,18 +994,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int half = warp >> 2, r = tid & (kTile - 1), row = q0 + r;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_off + half * 64, tp = ts + L::kDPCol;
-    const int vis = dense_visible(pb, len, row), all = dense_visible(pb, len, q0);
-    const long at = ((long)b * pb.H + h) * pb.Nq + row;
+    const int vis = dense_visible(pb, x.len, row), all = dense_visible(pb, x.len, q0);
+    const long at = ((long)x.b * pb.H + x.h) * pb.Nq + row;
     const bool live = row < pb.Nq && vis > 0;
     const float lse2 = live ? dense_lse2(__ldg(a.lse + at)) : INFINITY;
-    const float delta = !DELTA && live ? __ldg(a.delta + at) : 0.f;
-    float sum = 0.f;
     const float sl = pb.scale * kLog2e;
     const float2 sl2 = make_float2(sl, sl), base2 = make_float2(-lse2, -lse2);
-    const float2 nd2 = make_float2(-delta, -delta);
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = mbar_wait(s_full, j & 1, abort_flag, a.status))) break;
+    // d = P (dO V^T - delta) of step j, hidden keys zero; P and dP are read
+    auto weights = [&](int j, float2 nd2, float (&d)[64]) -> bool {
+      if (!mbar_wait(s_full, j & 1, abort_flag, a.status)) return false;
       tc_fence_after();
       float p[64];
       load_half(ts, p);
@@ -1036,9 +1013,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         p[e] = ex2(u.x);
         p[e + 1] = ex2(u.y);
       }
-      if (!(ok = mbar_wait(dp_full, j & 1, abort_flag, a.status))) break;
+      if (!mbar_wait(dp_full, j & 1, abort_flag, a.status)) return false;
       tc_fence_after();
-      float d[64];
       load_half(tp, d);
 #pragma unroll
       for (int e = 0; e < 64; e += 2) {
@@ -1047,29 +1023,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         d[e] = u.x;
         d[e + 1] = u.y;
       }
-      if ((j + 1) * kTile > all) {  // hidden keys, whatever the products hold
-        const int lim = vis - j * kTile - half * 64;
+      const int k0 = key_tile_of(j) * kTile;
+      if (k0 + kTile > all) {  // hidden keys, whatever the products hold
+        const int lim = vis - k0 - half * 64;
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e >= lim) d[e] = 0.f;
       }
-      if (DELTA) {
+      return true;
+    };
+    bool ok = true;
+    float delta = 0.f;
+    if (TWICE) {
+      float sum = 0.f;
+      for (int j = 0; j < n; ++j) {
+        float d[64];
+        if (!(ok = weights(j, make_float2(0.f, 0.f), d))) break;
 #pragma unroll
         for (int e = 0; e < 64; ++e) sum += d[e];
-      } else {
-        store_half(tp, d);
-        tmem_wait_st();
+        warp_arrive(ds_full);
       }
+      float* rows = reinterpret_cast<float*>(smem + L::kRowOff);
+      rows[half * kTile + r] = sum;
+      named_barrier(2, 2 * kTile);
+      delta = rows[r] + rows[kTile + r];
+      if (half == 0 && ok && row < pb.Nq) a.delta[at] = delta;
+    } else if (live) {
+      delta = __ldg(a.delta + at);
+    }
+    const float2 nd2 = make_float2(-delta, -delta);
+    for (int j = TWICE ? n : 0; j < steps && ok; ++j) {
+      float d[64];
+      if (!(ok = weights(j, nd2, d))) break;
+      store_half(tp, d);
+      tmem_wait_st();
       warp_arrive(ds_full);
     }
     if (ok && n > 0) ok = mbar_wait(done, 0, abort_flag, a.status);
     tc_fence_after();
-    if (DELTA) {
-      float* rows = reinterpret_cast<float*>(smem + L::kRowOff);
-      if (half == 1) rows[r] = sum;
-      named_barrier(1, 2 * kTile);
-      if (half == 0 && ok && row < pb.Nq) a.delta[at] = sum + rows[r];
-    } else if (half == 0) {
+    if (half == 0) {
       uint8_t* so = smem + L::kAOff;
       if (ok) {
         accumulator_row<D>(so, r, tmem + lane_off + L::kAccCol, pb.scale, n > 0);
@@ -1078,12 +1070,59 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       named_barrier(1, kTile);
       if (r == 0 && ok && !*abort_flag) {
         for (int c = 0; c < L::kCh; ++c)
-          if (c * 64 < pb.d) tma_store_4d(&mdq.map, so + c * kChunk, c * 64, q0, h, b);
+          if (c * 64 < pb.d) tma_store_4d(&mdq.map, so + c * kChunk, c * 64, q0, x.h, x.b);
         bulk_commit();
         bulk_wait_read<0>();
       }
     }
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    dense_dq_tc_kernel(const __grid_constant__ TileMap mq, const __grid_constant__ TileMap mk,
+                       const __grid_constant__ TileMap mv, const __grid_constant__ TileMap mg,
+                       const __grid_constant__ TileMap mdq, const __grid_constant__ BwdArgs a) {
+  using L = BwdLayout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) atomicExch(a.status, 2);
+    return;
+  }
+  const DenseProblem& pb = a.pb;
+  const int heads = pb.B * pb.H;
+  const int tile = pb.causal ? a.tiles - 1 - blockIdx.x / heads : blockIdx.x % a.tiles;
+  const int bh = pb.causal ? blockIdx.x % heads : blockIdx.x / a.tiles;
+  DqTile x;
+  x.h = bh % pb.H;
+  x.b = bh / pb.H;
+  x.hk = x.h / (pb.H / pb.Hkv);
+  x.q0 = tile * kTile;
+  x.len = dense_len(pb, x.b);
+  x.n = (dense_visible(pb, x.len, min(x.q0 + kTile, pb.Nq) - 1) + kTile - 1) / kTile;
+  x.tail = x.n * kTile > x.len && x.len < pb.Nk ? x.len - (x.n - 1) * kTile : kTile;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  if (tid == 0) {
+    for (int i = 0; i < 15; ++i)  // (as dq_tile names them)
+      mbar_init(bars + i, i == 11 || i == 13 ? 8 : 1);
+    *reinterpret_cast<volatile int*>(bars + 16) = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  if (x.n <= kExactTiles)
+    dq_tile<D, true>(smem, tmem, mq, mk, mv, mg, mdq, a, x, warp);
+  else
+    dq_tile<D, false>(smem, tmem, mq, mk, mv, mg, mdq, a, x, warp);
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -1153,31 +1192,31 @@ cudaError_t forward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, c
 template <int D>
 cudaError_t backward_d(const TileMap& mq, const TileMap& mk, const TileMap& mv, const TileMap& mg,
                        const TileMap& mdq, const TileMap& mdk, const TileMap& mdv, BwdArgs a,
-                       bool exact_delta, cudaStream_t stream, int* launches) {
+                       cudaStream_t stream, int* launches) {
   using L = BwdLayout<D>;
   cudaError_t e;
-  if (exact_delta) {
-    if ((e = allow_smem<dense_dq_tc_kernel<D, true>>(L::kBytes)) != cudaSuccess) return e;
+  auto dq = [&] {
+    if ((e = allow_smem<dense_dq_tc_kernel<D>>(L::kBytes)) != cudaSuccess) return e;
     a.tiles = (a.pb.Nq + kTile - 1) / kTile;
-    e = timed_launch("dense_delta_tc", stream, launches, [&] {
-      dense_dq_tc_kernel<D, true><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
-                                    stream>>>(mq, mk, mv, mg, mdq, a);
+    return timed_launch("dense_dq_tc", stream, launches, [&] {
+      dense_dq_tc_kernel<D><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
+                              stream>>>(mq, mk, mv, mg, mdq, a);
     });
-    if (e != cudaSuccess) return e;
-  }
-  if ((e = allow_smem<dense_dkv_tc_kernel<D>>(L::kBytes)) != cudaSuccess) return e;
-  a.tiles = (a.pb.Nk + kTile - 1) / kTile;
-  e = timed_launch("dense_dkv_tc", stream, launches, [&] {
-    dense_dkv_tc_kernel<D><<<(unsigned)a.tiles * a.pb.Hkv * a.pb.B, kBwdThreads, L::kBytes,
-                             stream>>>(mq, mk, mv, mg, mdk, mdv, a);
-  });
-  if (e != cudaSuccess) return e;
-  if ((e = allow_smem<dense_dq_tc_kernel<D, false>>(L::kBytes)) != cudaSuccess) return e;
-  a.tiles = (a.pb.Nq + kTile - 1) / kTile;
-  return timed_launch("dense_dq_tc", stream, launches, [&] {
-    dense_dq_tc_kernel<D, false><<<(unsigned)a.tiles * a.pb.H * a.pb.B, kBwdThreads, L::kBytes,
-                                   stream>>>(mq, mk, mv, mg, mdq, a);
-  });
+  };
+  auto dkv = [&] {
+    if ((e = allow_smem<dense_dkv_tc_kernel<D>>(L::kBytes)) != cudaSuccess) return e;
+    a.tiles = (a.pb.Nk + kTile - 1) / kTile;
+    return timed_launch("dense_dkv_tc", stream, launches, [&] {
+      dense_dkv_tc_kernel<D><<<(unsigned)a.tiles * a.pb.Hkv * a.pb.B, kBwdThreads, L::kBytes,
+                               stream>>>(mq, mk, mv, mg, mdk, mdv, a);
+    });
+  };
+  // dQ first where its short tiles give delta; else last, for dK and dV behind
+  // it take up to 7% longer (12 heads of 4680: 240 us, behind dQ 242 to 261,
+  // with where the tensors lie)
+  const bool dq_first = a.pb.Nk <= kExactTiles * kTile || a.pb.causal || a.pb.k_lens;
+  if ((e = dq_first ? dq() : dkv()) != cudaSuccess) return e;
+  return dq_first ? dkv() : dq();
 }
 
 }  // namespace
@@ -1226,20 +1265,14 @@ cudaError_t dense_tc_backward(const bf16* q, const bf16* k, const bf16* v, const
       !make_tile_map(&mdk, dk, pb.dk, pb.B, pb.Hkv, pb.Nk, pb.d) ||
       !make_tile_map(&mdv, dv, pb.dv, pb.B, pb.Hkv, pb.Nk, pb.d))
     return cudaErrorInvalidValue;
-  // delta = row sum of dO O = row sum of P (dO V^T).  Over few keys, the bf16
-  // rounding of O in the first shows in dQ and dK (36 causal keys: error 2.8e-3
-  // of them, 2.4e-3 with the second, of which the rounding of dS and of the
-  // result are the rest); the second takes two more products, which calls of
-  // this size do not feel.
-  const bool exact_delta = pb.Nk <= 512;
-  if (!exact_delta) {
+  if (pb.Nk > kExactTiles * kTile) {  // some tiles may be longer
     const cudaError_t e = dense_delta<bf16>(out, dout, delta, pb, stream, launches);
     if (e != cudaSuccess) return e;
   }
   const BwdArgs a = {lse, delta, pb, 0, status};
   return pb.d <= 64
-             ? backward_d<64>(mq, mk, mv, mg, mdq, mdk, mdv, a, exact_delta, stream, launches)
-             : backward_d<128>(mq, mk, mv, mg, mdq, mdk, mdv, a, exact_delta, stream, launches);
+             ? backward_d<64>(mq, mk, mv, mg, mdq, mdk, mdv, a, stream, launches)
+             : backward_d<128>(mq, mk, mv, mg, mdq, mdk, mdv, a, stream, launches);
 }
 
 }  // namespace monarch

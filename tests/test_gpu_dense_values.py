@@ -1,5 +1,5 @@
-"""Exact attention where values are not numbers, scores are infinite or pages lie
-outside the cache."""
+"""Exact attention where values are not numbers, scores are infinite, pages lie
+outside the cache or sums cancel."""
 import numpy as np
 import pytest
 import torch
@@ -136,3 +136,32 @@ def test_keys_of_bad_pages_are_zero(cuda_lib, keys, page, dtype):
     assert all(torch.equal(a, b) for a, b in zip(
         (out, lse), cuda_lib.monarch_attn_dense_decode(q, k, v, ref, lens)))
     cuda_lib.check()
+
+
+# --------------------------------------------------------------------------
+# values with a large common part
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nk,causal,lens", [(300, False, None), (600, False, [36, 600, 129]),
+                                            (700, True, None), (1100, True, [1100, 512, 90])])
+def test_gradients_of_rows_with_few_keys(cuda_lib, Nk, causal, lens, d):
+    """Values of 256 or 258: dO V^T - delta cancels all but the 2, and a delta
+    from out, rounded to a multiple of 2, would be off by as much.  Rows that
+    see up to 512 keys take it from the probabilities, however long the
+    tensors of their batch are."""
+    B = 1 if lens is None else len(lens)
+    q, k, v, do, kl = dense_case(B, 2, 1, Nk, Nk, d, causal, lens, "head", BF16)
+    v = 256 + 2 * (v > 0).to(BF16)
+    out, lse = cuda_lib.monarch_attn_dense_fwd(q, k, v, causal=causal, k_lens=kl)
+    dq, dk, _ = cuda_lib.monarch_attn_dense_bwd(q, k, v, out, lse, do, causal=causal, k_lens=kl)
+    cuda_lib.check()
+    x = [f64(t) for t in (q, k, v, do)]
+    # the keys that the last row of each row's tile of 128 sees
+    last = np.minimum(np.arange(Nk) // 128 * 128 + 127, Nk - 1)
+    sees = np.minimum(np.reshape([Nk] * B if lens is None else lens, (B, 1)),
+                      last + 1 if causal else Nk)
+    few = np.broadcast_to(sees <= 512, (B, Nk))[:, None]
+    refs = dense_ref.dense_backward(*x, causal, lens)
+    bounds = dense_ref.dense_errors(*x, half_step(BF16), causal, lens, exact_delta=few)
+    close("dq", dq, refs[0], bounds[2])
+    close("dk", dk, refs[1], bounds[3])
