@@ -326,8 +326,13 @@ def _workspace_need(call, device_index, *sizes):
 
 
 def _like(t):
-    """Uninitialised, t's shape, and t's strides unless its elements repeat."""
-    return t.new_empty(t.shape) if 0 in t.stride() else torch.empty_like(t)
+    """Uninitialised, t's shape, and t's strides unless its elements repeat
+    (of rows that overlap, torch may make another dimension the innermost)."""
+    if 0 not in t.stride():
+        y = torch.empty_like(t)
+        if y.stride(-1) == 1 or t.shape[-1] == 1:
+            return y
+    return t.new_empty(t.shape)
 
 
 def _dense_dims(q, k, v, scale):

@@ -1,6 +1,7 @@
 """Refusals of the exact-attention entry points that concern arguments beside
 q, k and v (fake pointers, as no device call is made).  CPU only."""
 import pytest
+import torch
 
 from structured_sub_quadratic_b200 import _build, api
 
@@ -36,3 +37,21 @@ def test_text_of_a_bad_index_says_what_the_kernels_do(lib):
     """Keys of a page outside the cache are zeros, and stay in the softmax."""
     text = lib.monarch_attn_strerror(api.MONARCH_ERR_BAD_INDEX)
     assert b"zero" in text and b"left out" not in text
+
+
+@pytest.mark.parametrize("shape,strides", [
+    ((1, 1, 3, 8), (100, 100, 1, 1)),      # windows that step by one channel
+    ((2, 1, 16, 8), (1, 100, 8, 1)),       # sequences that do
+    ((2, 3, 16, 8), (1, 1, 8, 1)),
+    ((2, 3, 16, 8), (384, 8, 24, 1)),      # token-major
+    ((2, 3, 16, 8), (0, 0, 8, 1)),         # broadcast
+    ((2, 3, 16, 1), (48, 16, 1, 7)),       # one channel
+])
+def test_results_have_contiguous_channels(shape, strides):
+    """Whatever the strides of an input, what is allocated like it can be written."""
+    t = torch.zeros(1000).as_strided(shape, strides)
+    y = api._like(t)
+    assert y.shape == t.shape and (y.stride(-1) == 1 or shape[-1] == 1)
+    # distinct elements
+    y.copy_(torch.arange(float(y.numel())).view(shape))
+    assert torch.equal(y.flatten(), torch.arange(float(y.numel())))

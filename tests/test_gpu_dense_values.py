@@ -1,5 +1,5 @@
 """Exact attention where values are not numbers, scores are infinite, pages lie
-outside the cache or sums cancel."""
+outside the cache, sums cancel or rows overlap."""
 import numpy as np
 import pytest
 import torch
@@ -165,3 +165,28 @@ def test_gradients_of_rows_with_few_keys(cuda_lib, Nk, causal, lens, d):
     bounds = dense_ref.dense_errors(*x, half_step(BF16), causal, lens, exact_delta=few)
     close("dq", dq, refs[0], bounds[2])
     close("dk", dk, refs[1], bounds[3])
+
+
+# --------------------------------------------------------------------------
+# layouts
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Nq,step", [(3, 1), (20, 8), (20, 3)])
+def test_rows_that_overlap(cuda_lib, Nq, step, dtype):
+    """Rows that are windows of one signal give what their copies give."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(4000, generator=g, device="cuda").to(dtype)
+    q, k, v = (x[o:].as_strided((1, 2, n, 32), (700, 350, step, 1))
+               for o, n in ((0, Nq), (1400, 25), (2800, 25)))
+    do = torch.randn(1, 2, Nq, 32, generator=g, device="cuda").to(dtype)
+    a = cuda_lib.monarch_attn_dense_fwd(q, k, v)
+    grads = cuda_lib.monarch_attn_dense_bwd(q, k, v, *a, do)
+    turned = cuda_lib.monarch_attn_rotary(q, grid=(Nq,))[0]
+    cuda_lib.check()
+    c = [t.contiguous() for t in (q, k, v)]
+    x = [f64(t) for t in (*c, do)]
+    refs = (*dense_ref.dense_forward(*x[:3]), *dense_ref.dense_backward(*x))
+    bounds = dense_ref.dense_errors(*x, half_step(dtype), rounded_weights=dtype is BF16)
+    for name, got, ref, bound in zip(("out", "lse", "dq", "dk", "dv"), (*a, *grads), refs, bounds):
+        close(name, got, ref, bound)
+    assert torch.equal(turned, cuda_lib.monarch_attn_rotary(c[0], grid=(Nq,))[0])
