@@ -1,5 +1,5 @@
 """Exact attention where values are not numbers, scores are infinite, pages lie
-outside the cache, sums cancel or rows overlap."""
+outside the cache, sums cancel, rows overlap or offsets pass 32 bits."""
 import numpy as np
 import pytest
 import torch
@@ -171,6 +171,21 @@ def test_gradients_of_rows_with_few_keys(cuda_lib, Nk, causal, lens, d):
 # layouts
 # --------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,Nq,Nk,causal", [(12, 300, 520, True), (24, 520, 130, False)])
+def test_one_key_head_for_many(cuda_lib, H, Nq, Nk, causal, dtype):
+    q, k, v, do, _ = dense_case(1, H, 1, Nq, Nk, 128, causal, None, "token", dtype)
+    out, lse = cuda_lib.monarch_attn_dense_fwd(q, k, v, causal=causal)
+    grads = cuda_lib.monarch_attn_dense_bwd(q, k, v, out, lse, do, causal=causal)
+    cuda_lib.check()
+    x = [f64(t) for t in (q, k, v, do)]
+    refs = (*dense_ref.dense_forward(*x[:3], causal), *dense_ref.dense_backward(*x, causal))
+    bounds = dense_ref.dense_errors(*x, half_step(dtype), causal, rounded_weights=dtype is BF16)
+    for name, got, ref, bound in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads), refs,
+                                     bounds):
+        close(name, got, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("Nq,step", [(3, 1), (20, 8), (20, 3)])
 def test_rows_that_overlap(cuda_lib, Nq, step, dtype):
     """Rows that are windows of one signal give what their copies give."""
@@ -190,3 +205,44 @@ def test_rows_that_overlap(cuda_lib, Nq, step, dtype):
     for name, got, ref, bound in zip(("out", "lse", "dq", "dk", "dv"), (*a, *grads), refs, bounds):
         close(name, got, ref, bound)
     assert torch.equal(turned, cuda_lib.monarch_attn_rotary(c[0], grid=(Nq,))[0])
+
+
+def far(t, dim):
+    """t in a buffer of its own where dimension `dim` steps so far that its last
+    entry starts above 2^31 elements."""
+    rest = list(t.shape)
+    n = rest.pop(dim)
+    strides = list(torch.empty(rest, device="meta").stride())
+    step = (2**31 // (n - 1) + 128) // 128 * 128
+    strides.insert(dim, step)
+    view = torch.empty(step * (n - 1) + t.numel(), device="cuda", dtype=t.dtype) \
+        .as_strided(t.shape, strides)
+    assert step * (n - 1) >= 2**31
+    return view.copy_(t)
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2])
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (F32, 64)])
+def test_offsets_above_32_bits(cuda_lib, dtype, d, dim):
+    q, k, v, do, _ = dense_case(2, 2, 2, 130, 140, d, True, None, "head", dtype)
+    ref = cuda_lib.monarch_attn_dense_fwd(q, k, v, causal=True)
+    grads = cuda_lib.monarch_attn_dense_bwd(q, k, v, *ref, do, causal=True)
+    turned = cuda_lib.monarch_attn_rotary(q, grid=(130,))[0]
+    fq, fk, fv, fo = (far(t, dim) for t in (q, k, v, q))
+    got = cuda_lib.monarch_attn_dense_fwd(fq, fk, fv, causal=True, out=fo)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    fg = cuda_lib.monarch_attn_dense_bwd(fq, fk, fv, *got, far(do, dim), causal=True)
+    assert all(torch.equal(a, b) for a, b in zip(fg, grads))
+    cuda_lib.monarch_attn_rotary(fq, grid=(130,), q_out=fo)
+    assert torch.equal(fo, turned)
+    cuda_lib.check()
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_cache_offsets_above_32_bits(cuda_lib, dtype, dim):
+    q, k, v, table, lens = decode_case(2, 4, 2, [100, 70], 16, 64, dtype, "head")
+    ref = cuda_lib.monarch_attn_dense_decode(q, k, v, table, lens)
+    got = cuda_lib.monarch_attn_dense_decode(q, far(k, dim), far(v, dim), table, lens)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    cuda_lib.check()
