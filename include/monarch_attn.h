@@ -266,9 +266,10 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
  * out = 0 and lse = -inf.  Keys past the length may hold anything (NaN
  * included); keys hidden by `causal` alone must be finite.  A visible score of
  * NaN or +inf makes its row NaN.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
- * for the product with v, sums are fp32.  fp32: operands are split into two
- * TF32 values and a product is off by 2^-20 of it at most; an infinity among
- * the visible values gives NaN.  scale > 0.  Few queries over many
+ * for the product with v, sums are fp32.  fp32 (and bf16 with d above 128 or no
+ * multiple of 8, or unaligned rows): operands are split into two TF32 values
+ * and a product is off by 2^-20 of it at most; an infinity among the visible
+ * values may give NaN where the exact result has none.  scale > 0.  Few queries over many
  * keys are split over the keys and joined in order; workspace: device,
  * 16-byte aligned, monarch_attn_dense_fwd_workspace_bytes (0 where nothing is
  * split). */
@@ -288,8 +289,10 @@ MONARCH_API size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int 
  * the rounding of out, relative to the values themselves, not to how they
  * differ from key to key).  strides: q, k, v, out,
  * dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
- * does a query without a visible key.  workspace: device, 16-byte aligned,
- * monarch_attn_dense_bwd_workspace_bytes. */
+ * does a query without a visible key.  q and dout have to be finite, in queries
+ * without a visible key too (their products have the weight 0); an infinite or
+ * NaN key or value makes the gradients that its products enter NaN.
+ * workspace: device, 16-byte aligned, monarch_attn_dense_bwd_workspace_bytes. */
 MONARCH_API int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* v,
                                        const void* out, const float* lse, const void* dout,
                                        void* dq, void* dk, void* dv, int B, int H, int Hkv,

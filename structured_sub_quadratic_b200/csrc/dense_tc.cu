@@ -166,8 +166,9 @@ __device__ __forceinline__ void accumulator_row(uint8_t* tile, int r, uint32_t t
 // fp32 sum), so rescaling O is rare.  A score of NaN or +inf makes the maximum
 // NaN, and with it the row's exponentials, sum and result.  P overwrites S, rounded to bf16 as the
 // result is, and is the A operand of P V.  Bound: the exponential unit and
-// the FMA pipe at d = 64 (800 TFLOP/s), the products at d = 128, 12 heads of
-// 4680 in 137 us (0.98 PFLOP/s).
+// the FMA pipe at d = 64 (12 heads of 16384 in 1047 us between idle times, 790
+// TFLOP/s, and 1127 in a pass among others, 730), the products at d = 128, 12
+// heads of 4680 in 139 us (0.97 PFLOP/s).
 // Warps: four of softmax per tile, one of TMA, one of products.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 64;  // keys of a step
@@ -523,8 +524,8 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
 // the first, 4-7 the second half), warp 8 issues TMA and warp 9 the products.
 // P and dS are rounded to bf16 as operands, half a step each like the results;
 // every sum is fp32.  Bound: the products and the chain score, exponential,
-// product between them; 12 heads of 4680 x 128: dK and dV 243 us (1.11
-// PFLOP/s of their products), dQ 175 us (1.15).
+// product between them; 12 heads of 4680 x 128: dK and dV 240 us (1.12
+// PFLOP/s of their products), dQ 177 us (1.14).
 // ---------------------------------------------------------------------------
 struct BwdArgs {
   const float* lse;
@@ -543,8 +544,10 @@ constexpr int kBwdThreads = 320;
 // against 2.4e-3, of which the roundings of dS and of the result are the rest).
 // So tiles of queries that see up to 512 keys take the second form, whatever the
 // length of the tensors that their sequence shares, at the price of two more
-// products (five in dQ, for three) and a second walk over their keys; longer
-// tiles take the first.
+// products (five in dQ, for three) and a second walk over their keys (32 x 12
+// heads of 197 x 64: 108 us, in a kernel of its own 122; 16 x 12 causal heads of
+// 640 x 64, most of whose tiles are short: 163 us, with the first form 148);
+// longer tiles take the first.
 constexpr int kExactTiles = 4;
 
 // The 64 columns of a thread as bf16 pairs, over its own half of a score tile.

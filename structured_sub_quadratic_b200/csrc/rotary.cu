@@ -8,8 +8,10 @@
 //
 // Angles are far too large for 32 bits (a position of 10^6 leaves 2^-4 rad).
 // A frequency is held as a fraction of a turn in units of 2^-64, so that
-// position * frequency modulo 2^64 is the angle reduced to one turn, off by
-// 2^-34 turns for any 32-bit position; its top 32 bits are the angle.
+// position * frequency modulo 2^64 is the angle reduced to one turn, off by less
+// than 2^-32 turns for any 32-bit position (the fraction is cut, 2^-64, and its
+// division rounded, 2^-66, for frequencies up to 1); its top 32 bits are the
+// angle.
 //
 // A thread keeps one place of one token (a unit: a pair, or 16-byte chunks of
 // pairs) and its cosines and sines in registers, and walks the heads of q and
