@@ -269,7 +269,8 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
  * for the product with v, sums are fp32.  fp32 (and bf16 with d above 128 or no
  * multiple of 8, or unaligned rows): operands are split into two TF32 values
  * and a product is off by 2^-20 of it at most; an infinity among the visible
- * values may give NaN where the exact result has none.  scale > 0.  Few queries over many
+ * values (a NaN whose upper ten bits of mantissa are zero counts as one) may
+ * give NaN where the exact result has none.  scale > 0.  Few queries over many
  * keys are split over the keys and joined in order; workspace: device,
  * 16-byte aligned, monarch_attn_dense_fwd_workspace_bytes (0 where nothing is
  * split). */
@@ -287,8 +288,9 @@ MONARCH_API size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int 
  * take the row sums of dout out from the probabilities instead of the rounded
  * out in tiles of 128 queries that see up to 512 keys; elsewhere dq and dk carry
  * the rounding of out, relative to the values themselves, not to how they
- * differ from key to key).  strides: q, k, v, out,
- * dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
+ * differ from key to key).  bf16: the probabilities and their gradients are
+ * rounded to bf16 for the products with dout, q and k, sums are fp32.  strides:
+ * q, k, v, out, dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
  * does a query without a visible key.  q and dout have to be finite, in queries
  * without a visible key too (their products have the weight 0); an infinite or
  * NaN key or value makes the gradients that its products enter NaN.
@@ -311,7 +313,9 @@ MONARCH_API size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq);
  * -inf, gets out = 0, lse = -inf; a score of NaN or +inf makes the head's NaN.
  * lse: (B, H).  strides: q (batch, head, unused), k_cache and v_cache (page,
  * head, row), out (batch, head, unused).  Rows of a page past the length may
- * hold anything.  The cache is split over its length and joined in order.  A
+ * hold anything.  bf16 with d a multiple of 8 up to 128 and aligned rows:
+ * probabilities are rounded to bf16 for the product with the values, sums are
+ * fp32.  The cache is split over its length and joined in order.  A
  * page index outside [0, n_pages) stands for zero keys and values (which score
  * 0 and keep their weight in the softmax), a length outside its range counts as
  * the nearer end, and monarch_attn_check then reports MONARCH_ERR_BAD_INDEX.  workspace: device, 16-byte aligned,
@@ -341,7 +345,7 @@ MONARCH_API size_t monarch_attn_dense_decode_workspace_bytes(int dtype, int B, i
  * (device, ints, (n_axes, N) contiguous per batch, batches
  * positions_batch_stride elements apart, 0 to share them); one of them is
  * NULL.  freqs: host, one angular frequency per pair, axis after axis; the
- * angles are reduced in 64 bits. */
+ * angles are reduced in 64 bits, their cosines and sines are off by 2^-21. */
 MONARCH_API int monarch_attn_rotary(int dtype, const void* q, const void* k, void* q_out,
                                     void* k_out, int B, int H, int Hkv, int N, int d,
                                     const long long* strides, int n_axes, const int* axis_dims,
