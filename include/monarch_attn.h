@@ -262,18 +262,18 @@ MONARCH_API int monarch_attn_bwd(int dtype, const void* q, const void* k, const 
  * head h reads head h / (H / Hkv)); strides: q, k, v, out.  Key j is visible
  * to query i of batch b when j < k_lens[b] (device, B ints, or NULL; values
  * outside [0, Nk] count as the nearer end) and, if causal, j <= i + Nk - Nq.
- * A row without a visible key, or whose visible keys all score -inf, gets
- * out = 0 and lse = -inf.  Keys past the length may hold anything (NaN
- * included); keys hidden by `causal` alone must be finite.  A visible score of
- * NaN or +inf makes its row NaN.  Nq and Nk may be 0.  bf16: probabilities are rounded to bf16
- * for the product with v, sums are fp32.  fp32 (and bf16 with d above 128 or no
- * multiple of 8, or unaligned rows): operands are split into two TF32 values
- * and a product is off by 2^-20 of it at most; an infinity among the visible
- * values (a NaN whose upper ten bits of mantissa are zero counts as one) may
- * give NaN where the exact result has none.  scale > 0.  Few queries over many
- * keys are split over the keys and joined in order; workspace: device,
- * 16-byte aligned, monarch_attn_dense_fwd_workspace_bytes (0 where nothing is
- * split). */
+ * A row without a visible key, or whose visible keys all score -inf, gets out
+ * = 0 and lse = -inf.  Keys past the length may hold anything (NaN included);
+ * keys hidden by `causal` alone must be finite.  A visible score of NaN or
+ * +inf makes its row NaN.  Nq and Nk may be 0.  bf16: probabilities are
+ * rounded to bf16 for the product with v, sums are fp32.  fp32 (and bf16 with
+ * d above 128 or no multiple of 8, or unaligned rows): operands are split into
+ * two TF32 values and a product is off by 2^-20 of it at most; an infinity
+ * among the visible values (a NaN whose upper ten bits of mantissa are zero
+ * counts as one) may give NaN where the exact result has none.  scale > 0.  Few
+ * queries over many keys are split over the keys and joined in order;
+ * workspace: device, 16-byte aligned, monarch_attn_dense_fwd_workspace_bytes (0
+ * where nothing is split). */
 MONARCH_API int monarch_attn_dense_fwd(int dtype, const void* q, const void* k, const void* v,
                                        void* out, float* lse, int B, int H, int Hkv, int Nq,
                                        int Nk, int d, const long long* strides, int causal,
@@ -283,18 +283,19 @@ MONARCH_API size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int 
                                                           int d);
 
 /* Gradients of sum(out * dout) with respect to q, k and v; the probabilities
- * are recomputed from q, k and lse.  out and lse: what
- * monarch_attn_dense_fwd gave for the same arguments (the tensor-core kernels
- * take the row sums of dout out from the probabilities instead of the rounded
- * out in tiles of 128 queries that see up to 512 keys; elsewhere dq and dk carry
- * the rounding of out, relative to the values themselves, not to how they
- * differ from key to key).  bf16: the probabilities and their gradients are
- * rounded to bf16 for the products with dout, q and k, sums are fp32.  strides:
- * q, k, v, out, dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
- * does a query without a visible key.  q and dout have to be finite, in queries
- * without a visible key too (their products have the weight 0); an infinite or
- * NaN key or value makes the gradients that its products enter NaN.
- * workspace: device, 16-byte aligned, monarch_attn_dense_bwd_workspace_bytes. */
+ * are recomputed from q, k and lse.  out and lse: what monarch_attn_dense_fwd
+ * gave for the same arguments (the tensor-core kernels take the row sums of
+ * dout out from the probabilities instead of the rounded out in tiles of 128
+ * queries that see up to 512 keys; elsewhere dq and dk carry the rounding of
+ * out, relative to the values themselves, not to how they differ from key to
+ * key).  bf16: the probabilities P and dS = P (dP - row sum) are rounded to
+ * bf16 for the products with dout, q and k, sums are fp32.  strides: q, k,
+ * v, out, dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
+ * does a query without a visible key.  q and dout have to be finite, in
+ * queries without a visible key too (their products have the weight 0); an
+ * infinite or NaN key or value makes the gradients that its products enter
+ * NaN.  workspace: device, 16-byte aligned,
+ * monarch_attn_dense_bwd_workspace_bytes. */
 MONARCH_API int monarch_attn_dense_bwd(int dtype, const void* q, const void* k, const void* v,
                                        const void* out, const float* lse, const void* dout,
                                        void* dq, void* dk, void* dv, int B, int H, int Hkv,
@@ -315,10 +316,11 @@ MONARCH_API size_t monarch_attn_dense_bwd_workspace_bytes(int B, int H, int Nq);
  * head, row), out (batch, head, unused).  Rows of a page past the length may
  * hold anything.  bf16 with d a multiple of 8 up to 128 and aligned rows:
  * probabilities are rounded to bf16 for the product with the values, sums are
- * fp32.  The cache is split over its length and joined in order.  A
- * page index outside [0, n_pages) stands for zero keys and values (which score
- * 0 and keep their weight in the softmax), a length outside its range counts as
- * the nearer end, and monarch_attn_check then reports MONARCH_ERR_BAD_INDEX.  workspace: device, 16-byte aligned,
+ * fp32.  The cache is split over its length and joined in order.  A page index
+ * outside [0, n_pages) stands for zero keys and values (which score 0 and keep
+ * their weight in the softmax), a length outside its range counts as the
+ * nearer end, and monarch_attn_check then reports MONARCH_ERR_BAD_INDEX.
+ * workspace: device, 16-byte aligned,
  * monarch_attn_dense_decode_workspace_bytes. */
 MONARCH_API int monarch_attn_dense_decode(int dtype, const void* q, const void* k_cache,
                                           const void* v_cache, const int* page_table,
