@@ -290,8 +290,8 @@ MONARCH_API size_t monarch_attn_dense_fwd_workspace_bytes(int dtype, int B, int 
  * out, relative to the values themselves, not to how they differ from key to
  * key).  bf16: the probabilities P and dS = P (dP - row sum) are rounded to
  * bf16 for the products with dout, q and k, sums are fp32.  strides: q, k,
- * v, out, dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and so
- * does a query without a visible key.  q and dout have to be finite, in
+ * v, out, dout, dq, dk, dv.  A key that no query sees gets a gradient of 0, and
+ * so does a query without a visible key.  q and dout have to be finite, in
  * queries without a visible key too (their products have the weight 0); an
  * infinite or NaN key or value makes the gradients that its products enter
  * NaN.  workspace: device, 16-byte aligned,

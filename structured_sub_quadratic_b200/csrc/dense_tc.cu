@@ -157,15 +157,15 @@ __device__ __forceinline__ void accumulator_row(uint8_t* tile, int r, uint32_t t
 // (where two CTAs share an SM: their softmaxes drift apart, which those of one
 // CTA's tiles do not, 12 heads of 16384 keys 1075 -> 1022 us), a warpgroup each
 // with a thread per row.  They walk the keys 64 at a time in one pass.  S has
-// two buffers a tile, so that S of step u + 2 is issued right behind P V of
-// step u and the softmaxes never wait for a product that has not long begun
-// (with one 128-key buffer, the chain softmax, P V, S took 3450 clocks per 256
-// x 128 scores at d = 128, against 2070 of products).  O stays in TMEM
-// under a running maximum that only moves when it grows by more than 2^8
-// (probabilities then reach 256, exact in the exponents of P's bf16 and of the
-// fp32 sum), so rescaling O is rare.  A score of NaN or +inf makes the maximum
-// NaN, and with it the row's exponentials, sum and result.  P overwrites S, rounded to bf16 as the
-// result is, and is the A operand of P V.  Bound: the exponential unit and
+// two buffers a tile, so that S of step u + 2 is issued right behind P V of step
+// u and the softmaxes never wait for a product that has not long begun (with one
+// 128-key buffer, the chain softmax, P V, S took 3450 clocks per 256 x 128
+// scores at d = 128, against 2070 of products).  O stays in TMEM under a running
+// maximum that only moves when it grows by more than 2^8 (probabilities then
+// reach 256, exact in the exponents of P's bf16 and of the fp32 sum), so
+// rescaling O is rare.  A score of NaN or +inf makes the maximum NaN, and with
+// it the row's exponentials, sum and result.  P overwrites S, rounded to bf16 as
+// the result is, and is the A operand of P V.  Bound: the exponential unit and
 // the FMA pipe at d = 64 (12 heads of 16384 in 1047 us between idle times, 790
 // TFLOP/s, and 1127 in a pass among others, 730), the products at d = 128, 12
 // heads of 4680 in 139 us (0.97 PFLOP/s).
@@ -517,15 +517,15 @@ __global__ void __launch_bounds__(FwdLayout<D>::kThreads, 3 - FwdLayout<D>::kTil
 
 // ---------------------------------------------------------------------------
 // Backward.  The probabilities are recomputed from q, k and lse; delta is the
-// row sum of dO O, from one form of it or another (kExactTiles).  Two kernels, so that no sum needs atomics: one owns a tile
-// of keys and walks the queries (dK, dV: four products a tile), the other a
-// tile of queries and walks the keys (dQ: three).  In both, eight warps hold
-// the score tile with two threads per TMEM lane (64 columns each: warps 0-3
-// the first, 4-7 the second half), warp 8 issues TMA and warp 9 the products.
-// P and dS are rounded to bf16 as operands, half a step each like the results;
-// every sum is fp32.  Bound: the products and the chain score, exponential,
-// product between them; 12 heads of 4680 x 128: dK and dV 240 us (1.12
-// PFLOP/s of their products), dQ 177 us (1.14).
+// row sum of dO O, from one form of it or another (kExactTiles).  Two kernels,
+// so that no sum needs atomics: one owns a tile of keys and walks the queries
+// (dK, dV: four products a tile), the other a tile of queries and walks the keys
+// (dQ: three).  In both, eight warps hold the score tile with two threads per
+// TMEM lane (64 columns each: warps 0-3 the first, 4-7 the second half), warp 8
+// issues TMA and warp 9 the products.  P and dS are rounded to bf16 as operands,
+// half a step each like the results; every sum is fp32.  Bound: the products and
+// the chain score, exponential, product between them; 12 heads of 4680 x 128: dK
+// and dV 240 us (1.12 PFLOP/s of their products), dQ 177 us (1.14).
 // ---------------------------------------------------------------------------
 struct BwdArgs {
   const float* lse;
